@@ -83,7 +83,8 @@ typedef enum {
   TQ_ERR_INTERNAL = 6
 } tq_status;
 
-typedef enum { TQ_F32 = 0, TQ_BF16 = 1 } tq_dtype;
+/* TQ_F16 is taken by the paged-cache and prompt calls only. */
+typedef enum { TQ_F32 = 0, TQ_BF16 = 1, TQ_F16 = 2 } tq_dtype;
 
 /* How values are stored. */
 typedef enum {
@@ -100,6 +101,10 @@ typedef enum {
 /* Bits of the sticky per-device error word (tq_device_errors). */
 #define TQ_ERRF_DECODE_WAIT 1u   /* a decode kernel gave up on a bounded wait */
 #define TQ_ERRF_QUANTIZE_WAIT 2u /* a quantize-append kernel gave up on one */
+#define TQ_ERRF_PAGE 4u     /* a paged call met a page number outside the pool, or a
+                               position outside its block-table row */
+#define TQ_ERRF_POSITION 8u /* tq_paged_append met a position outside the rotation table */
+#define TQ_ERRF_PROMPT_WAIT 16u /* tq_prompt_attention gave up on a bounded wait */
 
 /* Tokens per cache tile; capacity must be a multiple of it. */
 #define TQ_TILE_TOKENS 128
@@ -475,6 +480,197 @@ TQ_API tq_status tq_device_errors(uint32_t *flags, int clear);
 TQ_API tq_status tq_dequantize(const tq_params *p, const tq_cache *c, int b,
                         int start, int count, float *k_out, float *v_out,
                         tq_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 4-bit cache
+ *
+ * A pool of fixed-size pages shared by all sequences of a layer, addressed
+ * through a block table, with keys and values both held in the library's
+ * min/max value codec at 4 bits ("turboquant/audit_claims.py", AUDIT 1:
+ * value_bits, value_group_size): per group of 32 channels
+ *   zero = fp16(min), scale = fp16((max - min) / 15),
+ *   code = clamp(rint((x - zero) / scale), 0, 15)   (half to even; 0 where
+ *   scale is 0),   value = code * scale + zero.
+ * It needs no rotation matrix, sketch or codebook: the plain cache to put a
+ * TurboQuant cache next to, and the one for keys whose position rotation is
+ * applied on the way in.
+ *
+ * The calls take lengths and block tables from device memory, so a captured
+ * CUDA graph of them follows a batch as it grows; what the host cannot check
+ * is checked in the kernels: a page number outside [0, num_pages), or a
+ * position outside the block-table row, is never dereferenced (append skips
+ * the token, gather and decode return NaN rows for it) and sets TQ_ERRF_PAGE.
+ * Groups with a NaN or an infinity decode to NaN; magnitudes above the fp16
+ * range (65504) are not representable.
+ * ------------------------------------------------------------------------ */
+
+/* Largest query heads per KV head of the paged decode and the prompt call. */
+#define TQ_PAGED_MAX_GQA 8
+
+/*
+ * One layer's page pool.
+ *   d            64, 128 or 256
+ *   page_tokens  tokens per page: a power of two, 16..1024
+ *   data         device, tq_paged_bytes() bytes, 256-byte aligned
+ * Layout: page p starts at byte p * h_kv * (page_tokens / 16) * 20 d and
+ * holds, for each KV head, page_tokens / 16 cells of 16 tokens.  A cell is
+ * 20 d bytes, with G = d / 32 groups and P = min(G, 4): key codes [8 d],
+ * value codes [8 d], key scales, key zeros, value scales, value zeros (16 G
+ * fp16 each).  Token n = 8 s + 2 t + e (s, e in 0..1, t in 0..3) and channel
+ * c = 32 j + r of the cell lie at
+ *   key code    byte (j/P) 256 P + n 16 P + (r/8) 4 P + (j%P) 4 + (r%8)/2,
+ *               low half for even r
+ *   value code  byte (j/P) 256 P + s 128 P + ((r/4) 4 + t) 4 P + (j%P) 4
+ *               + 2 e + (r%4)/2, low half for even r
+ *   key zero    half n G + j of its section
+ *   the others  half t 4 G + j 4 + s 2 + e of their sections
+ * (the order in which the lanes of a warp take matrix operands).
+ * Slots that no token was written to may hold anything.
+ */
+typedef struct {
+  int d, h_kv, page_tokens, num_pages;
+  void *data;
+} tq_paged_cache;
+
+/*
+ * The sequences of a call.
+ *   len          device, [batch] int32: tokens of each sequence, those that
+ *                the call appends included (so one array serves the append
+ *                and the decode of a step)
+ *   block_table  device, [batch] rows of max_pages int32, table_stride apart:
+ *                page block_table[b][p / page_tokens] holds position p
+ */
+typedef struct {
+  int batch, max_pages, table_stride;
+  const int32_t *len;
+  const int32_t *block_table;
+} tq_paged_batch;
+
+/*
+ * Position rotation.  Row p of `table` (device, [max_positions][rotary_dim]
+ * fp32, 16-byte aligned) holds rotary_dim / 2 cosines, then as many sines;
+ * pair j of a head's first rotary_dim channels, (j, j + rotary_dim / 2), or
+ * (2 j, 2 j + 1) where `interleaved` is nonzero, turns by that angle:
+ *   a' = a cos - b sin,   b' = b cos + a sin,
+ * each formed in 64 bits and rounded once to 32 (so that the stored codes do
+ * not depend on the order of operations), then to the output's type.
+ * rotary_dim: a multiple of 16, 16..d.
+ */
+typedef struct {
+  int rotary_dim, max_positions, interleaved;
+  const float *table;
+} tq_rope;
+
+/*
+ * tq_make_rope_table -- host only: the table above for angles
+ * p * theta^(-2 j / rotary_dim), computed in double precision.
+ *   table  host, [max_positions][rotary_dim] floats
+ * TQ_ERR_INVALID_ARGUMENT for a null pointer, max_positions < 1 or a theta
+ * that is not positive and finite; TQ_ERR_UNSUPPORTED for rotary_dim.
+ */
+TQ_API tq_status tq_make_rope_table(int max_positions, int rotary_dim, double theta, float *table);
+
+/* Bytes of a page pool, or 0 for bad arguments. */
+TQ_API size_t tq_paged_bytes(int d, int h_kv, int page_tokens, int num_pages);
+
+/*
+ * tq_paged_append -- rotate and store the new tokens of every sequence.
+ *
+ *   rope        NULL: keys and queries are stored and copied unrotated
+ *   cu_new      device, [batch + 1] int32, ascending from 0: tokens
+ *               cu_new[b] .. cu_new[b + 1] - 1 of q, k and v are sequence
+ *               b's last ones, at positions len[b] - n_b .. len[b] - 1
+ *   q, k, v     device, T tokens of h_q, h_kv, h_kv rows of d, `dtype` (F32,
+ *               BF16 or F16); a token's rows are contiguous and tokens are
+ *               q_stride, k_stride, v_stride elements apart (the parts of one
+ *               projection's output can be passed as they lie); 16-byte
+ *               aligned, strides a multiple of 16 bytes.  q may be NULL.
+ *   T           rows of q, k and v; rows at or behind cu_new[batch] are
+ *               ignored
+ *   q_out, k_out  device or NULL: the rotated queries and keys in `dtype`,
+ *               laid out like q and k with their own strides; q_out may be
+ *               q, and k_out may be k (same stride)
+ * A position at or beyond max_positions stores nothing for its token, writes
+ * NaN rows to q_out and k_out and sets TQ_ERRF_POSITION; a token with no page
+ * stores nothing and sets TQ_ERRF_PAGE.  Tokens of one call are written once
+ * each; two sequences that name the same page must not append to it.
+ * Errors: TQ_ERR_INVALID_ARGUMENT (null or misaligned pointers, negative
+ * sizes, h_q not a multiple of h_kv, q without q_out), TQ_ERR_UNSUPPORTED (d,
+ * page_tokens, rotary_dim, dtype).
+ */
+TQ_API tq_status tq_paged_append(const tq_paged_cache *c, const tq_paged_batch *s, const tq_rope *rope,
+                                 const int32_t *cu_new, const void *q, const void *k, const void *v, tq_dtype dtype,
+                                 int h_q, int T, long long q_stride, long long k_stride, long long v_stride,
+                                 void *q_out, void *k_out, long long q_out_stride, long long k_out_stride,
+                                 tq_stream_t stream);
+
+/*
+ * tq_paged_gather -- the cached values of consecutive tokens, as contiguous
+ * rows (the history that tq_prompt_attention of a later chunk reads).
+ *
+ *   cu_rows  device, [batch + 1] int32, ascending from 0: rows cu_rows[b] ..
+ *            cu_rows[b + 1] - 1 receive sequence b's tokens from position
+ *            first[b] on
+ *   first    device, [batch] int32, or NULL for 0
+ *   rows     rows of k_out and v_out; those at or behind cu_rows[batch] are
+ *            left as they are
+ *   k_out, v_out  device, [rows][h_kv][d], `dtype` (F32, BF16 or F16), rows
+ *            k_stride, v_stride elements apart, 16-byte aligned, strides a
+ *            multiple of 16 bytes
+ * A row whose position is not below len[b], or whose page is bad, is NaN and
+ * sets TQ_ERRF_PAGE.  Errors as for tq_paged_append.
+ */
+TQ_API tq_status tq_paged_gather(const tq_paged_cache *c, const tq_paged_batch *s, const int32_t *cu_rows,
+                                 const int32_t *first, int rows, void *k_out, void *v_out, tq_dtype dtype,
+                                 long long k_stride, long long v_stride, tq_stream_t stream);
+
+/* Workspace bytes of tq_paged_decode_attention (0 for bad arguments). */
+TQ_API size_t tq_paged_decode_workspace_size(const tq_paged_cache *c, int batch, int h_q);
+
+/*
+ * tq_paged_decode_attention -- one query token per sequence over its cached
+ * tokens [0, len[b]), split over all of the batch's tokens and merged.
+ *
+ *   q, out     device, [batch][h_q][d], `dtype` (BF16 or F16; rounded once),
+ *              a sequence's rows contiguous, sequences q_stride, out_stride
+ *              elements apart, 16-byte aligned, strides a multiple of 16 bytes
+ *   h_q        a multiple of h_kv, at most TQ_PAGED_MAX_GQA times it; query
+ *              head hq reads KV head hq / (h_q / h_kv)
+ *   workspace  device, tq_paged_decode_workspace_size() bytes, 256-byte
+ *              aligned, no initialisation; one per call in flight
+ * A sequence with no tokens gets a zero row, one with a bad page NaN rows.
+ * Lengths beyond max_pages * page_tokens are bad pages.
+ */
+TQ_API tq_status tq_paged_decode_attention(const tq_paged_cache *c, const tq_paged_batch *s, const void *q,
+                                           tq_dtype dtype, int h_q, long long q_stride, float softmax_scale, void *out,
+                                           long long out_stride, void *workspace, size_t workspace_bytes,
+                                           tq_stream_t stream);
+
+/*
+ * tq_prompt_attention -- causal attention of packed sequences over contiguous
+ * keys and values.  Sequence b's queries are rows cu_q[b] .. cu_q[b + 1] - 1
+ * of q, its keys rows cu_k[b] .. cu_k[b + 1] - 1 of k and v; its query i (of
+ * n_q) sees keys j <= i + n_k - n_q: the last query sees every key, as for a
+ * chunk behind a history.  A query that sees no key gets a zero row.
+ *
+ *   q, out    device, [T_q][h_q][d], rows q_stride, out_stride elements apart
+ *   k, v      device, [T_k][h_kv][d], rows k_stride, v_stride apart
+ *             all `dtype` (BF16 or F16), 16-byte aligned, strides a multiple
+ *             of 16 bytes
+ *   h_q, h_kv, d   as for tq_paged_decode_attention
+ *   cu_q, cu_k     device, [batch + 1] int32, ascending from 0, at most T_q
+ *                  and T_k (values outside are clamped); the same array may
+ *                  serve both
+ * Rows of q at or behind cu_q[batch] are ignored and their rows of out are
+ * left as they are.  Keys and values of other sequences and those behind
+ * cu_k[batch] never reach a result, whatever they hold.  Within a sequence a
+ * NaN or an infinity in the value row of a key may also reach queries up to
+ * 127 positions before it.
+ */
+TQ_API tq_status tq_prompt_attention(const void *q, const void *k, const void *v, tq_dtype dtype, int T_q, int T_k,
+                                     int h_q, int h_kv, int d, long long q_stride, long long k_stride,
+                                     long long v_stride, const int32_t *cu_q, const int32_t *cu_k, int batch,
+                                     float softmax_scale, void *out, long long out_stride, tq_stream_t stream);
 
 #ifdef __cplusplus
 } /* extern "C" */

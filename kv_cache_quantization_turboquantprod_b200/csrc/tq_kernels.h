@@ -188,4 +188,11 @@ tq_status decode_common(const tq_params *p, const tq_cache *c, const void *q, tq
                         size_t workspace_bytes, cudaStream_t stream, bool validate_only = false);
 cudaError_t launch_dequantize(const DequantArgs &a, cudaStream_t stream);
 
+// Of the current device: its SM count, and the address of its sticky error
+// word (both cached per device).
+cudaError_t device_sm_count(int *out);
+cudaError_t device_error_word(unsigned int **out);
+// The bounded waits' limit (tq_set_wait_limit_ns).
+unsigned long long wait_limit_ns();
+
 }  // namespace tq

@@ -21,7 +21,7 @@ TQ_OK = 0
 STATUS = {0: "TQ_OK", 1: "TQ_ERR_INVALID_ARGUMENT", 2: "TQ_ERR_UNSUPPORTED",
           3: "TQ_ERR_CAPACITY", 4: "TQ_ERR_WORKSPACE", 5: "TQ_ERR_CUDA",
           6: "TQ_ERR_INTERNAL"}
-TQ_F32, TQ_BF16 = 0, 1
+TQ_F32, TQ_BF16, TQ_F16 = 0, 1, 2
 TQ_VALUES_GROUP, TQ_VALUES_MSE = 0, 1
 TILE_TOKENS = 128
 MAX_BATCH = 1024
@@ -32,8 +32,10 @@ EXPORTS = ("tq_status_string", "tq_make_codebook", "tq_record_bytes", "tq_cache_
            "tq_dequantize", "tq_decode_attention_noalloc", "tq_decode_attention_window",
            "tq_prefill_workspace_size", "tq_prefill_attention", "tq_prefill_tokens_per_pass",
            "tq_set_wait_limit_ns", "tq_device_errors", "tq_test_withhold_handoffs",
-           "tq_test_sign_refine_threshold", "tq_test_refine_count", "tq_sketch_product", "tq_prepare_operands")
-ERRF_DECODE_WAIT, ERRF_QUANTIZE_WAIT = 1, 2
+           "tq_test_sign_refine_threshold", "tq_test_refine_count", "tq_sketch_product", "tq_prepare_operands",
+           "tq_make_rope_table", "tq_paged_bytes", "tq_paged_append", "tq_paged_gather", "tq_paged_decode_workspace_size",
+           "tq_paged_decode_attention", "tq_prompt_attention")
+ERRF_DECODE_WAIT, ERRF_QUANTIZE_WAIT, ERRF_PAGE, ERRF_POSITION, ERRF_PROMPT_WAIT = 1, 2, 4, 8, 16
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
 
@@ -58,6 +60,21 @@ TQ_TC_OPERAND_BYTES = 5 * 128 * 128 * 2
 class Cache(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int), ("h_kv", ctypes.c_int),
                 ("capacity", ctypes.c_int), ("data", ctypes.c_void_p)]
+
+
+class _PagedCacheStruct(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int), ("h_kv", ctypes.c_int), ("page_tokens", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("data", ctypes.c_void_p)]
+
+
+class _PagedBatchStruct(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("max_pages", ctypes.c_int), ("table_stride", ctypes.c_int),
+                ("len", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+
+
+class _RopeStruct(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("max_positions", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("table", ctypes.c_void_p)]
 
 
 _lib = None
@@ -107,6 +124,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.tq_prefill_attention.argtypes = [P, C, vp, ci, ci, ci, vp, ci, ctypes.c_float, vp, vp, sz, vp]
     lib.tq_dequantize.restype = ci
     lib.tq_dequantize.argtypes = [P, C, ci, ci, ci, vp, vp, vp]
+    cll = ctypes.c_longlong
+    PC, PB, PR = (ctypes.POINTER(t) for t in (_PagedCacheStruct, _PagedBatchStruct, _RopeStruct))
+    lib.tq_make_rope_table.restype = ci
+    lib.tq_make_rope_table.argtypes = [ci, ci, ctypes.c_double, vp]
+    lib.tq_paged_bytes.restype = sz
+    lib.tq_paged_bytes.argtypes = [ci, ci, ci, ci]
+    lib.tq_paged_append.restype = ci
+    lib.tq_paged_append.argtypes = [PC, PB, PR, vp, vp, vp, vp, ci, ci, ci, cll, cll, cll, vp, vp, cll, cll, vp]
+    lib.tq_paged_gather.restype = ci
+    lib.tq_paged_gather.argtypes = [PC, PB, vp, vp, ci, vp, vp, ci, cll, cll, vp]
+    lib.tq_paged_decode_workspace_size.restype = sz
+    lib.tq_paged_decode_workspace_size.argtypes = [PC, ci, ci]
+    lib.tq_paged_decode_attention.restype = ci
+    lib.tq_paged_decode_attention.argtypes = [PC, PB, vp, ci, ci, cll, ctypes.c_float, vp, cll, vp, sz, vp]
+    lib.tq_prompt_attention.restype = ci
+    lib.tq_prompt_attention.argtypes = [vp, vp, vp, ci, ci, ci, ci, ci, ci, cll, cll, cll, vp, vp, ci,
+                                        ctypes.c_float, vp, cll, vp]
     lib.tq_set_wait_limit_ns.restype = ci
     lib.tq_set_wait_limit_ns.argtypes = [ctypes.c_ulonglong]
     lib.tq_test_withhold_handoffs.restype = ci
@@ -448,3 +482,212 @@ def workspace_for(layer: Layer, cache: CompressedCache, h_q: int, max_len: int,
     if n == 0:
         raise TQError("tq_decode_workspace_size", 1)
     return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+# ---------------------------------------------------------------------------
+# paged 4-bit cache and prompt attention
+# ---------------------------------------------------------------------------
+_PAGED_DTYPES = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+_HALF_DTYPES = {torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
+
+
+def _token_rows(name: str, t: torch.Tensor, heads: int | None, d: int, dtype, device, rows: int | None = None) -> int:
+    """Check [rows, heads, d] token rows whose heads are contiguous (tokens may lie further apart); returns the tokens'
+    stride in elements."""
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'tokens' if rows is None else rows}, {'heads' if heads is None else heads}, {d}], "
+                         f"got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    stride, by_head, by_channel = t.stride()
+    h = t.shape[1]
+    if by_channel != 1 or (by_head != d and h > 1):
+        raise ValueError(f"{name}: a token's heads must be contiguous rows")
+    return stride if t.shape[0] > 1 else max(stride, h * d)
+
+
+def _int32(name: str, t: torch.Tensor, n: int, device) -> int:
+    if t.dtype != torch.int32 or tuple(t.shape) != (n,) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {device}")
+    return t.data_ptr()
+
+
+def _on(device, stream, call):
+    """call(stream handle) with `device` current: its kernels run there whatever device the caller has selected."""
+    if torch.cuda.current_device() == device.index:
+        return call(torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
+    with torch.cuda.device(device):
+        return call(torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
+
+
+def tq_make_rope_table(max_positions: int, rotary_dim: int, theta: float = 10000.0) -> torch.Tensor:
+    """Host table [max_positions, rotary_dim] float32: cosines, then sines, of the angles p theta^(-2 j / rotary_dim)."""
+    table = torch.empty(max(int(max_positions), 1), max(int(rotary_dim), 1), dtype=torch.float32)
+    _check("tq_make_rope_table", load().tq_make_rope_table(int(max_positions), int(rotary_dim), float(theta), table.data_ptr()))
+    return table
+
+
+def tq_paged_bytes(d: int, h_kv: int, page_tokens: int, num_pages: int) -> int:
+    return int(load().tq_paged_bytes(d, h_kv, page_tokens, num_pages))
+
+
+class PagedCache:
+    """A pool of 4-bit pages (include/tq.h, tq_paged_cache) in a caller-owned uint8 tensor; allocated where none is given."""
+
+    def __init__(self, d: int, h_kv: int, page_tokens: int, num_pages: int, buffer: torch.Tensor | None = None, device="cuda"):
+        n = tq_paged_bytes(d, h_kv, page_tokens, num_pages)
+        if n == 0:
+            raise TQError("tq_paged_bytes", 1)
+        if buffer is None:
+            buffer = torch.empty(n, dtype=torch.uint8, device=device)
+        if buffer.dtype != torch.uint8 or not buffer.is_contiguous() or buffer.numel() < n or not buffer.is_cuda:
+            raise ValueError(f"buffer must be a contiguous CUDA uint8 tensor of at least {n} bytes")
+        self.buffer, self.device = buffer, buffer.device
+        self.d, self.h_kv, self.page_tokens, self.num_pages = d, h_kv, page_tokens, num_pages
+        self.struct = _PagedCacheStruct(d, h_kv, page_tokens, num_pages, buffer.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+
+class PagedBatch:
+    """Lengths [B] int32 (the tokens that a call appends included) and block table [B, max_pages] int32 on the device.
+    The tensors are read when a call's kernels run, so a loop updates them in place."""
+
+    def __init__(self, len_dev: torch.Tensor, block_table: torch.Tensor):
+        if len_dev.dim() != 1 or block_table.dim() != 2 or block_table.shape[0] != len_dev.shape[0]:
+            raise ValueError("len_dev must be [B] and block_table [B, max_pages]")
+        if len_dev.dtype != torch.int32 or block_table.dtype != torch.int32:
+            raise TypeError("len_dev and block_table must be int32")
+        if not len_dev.is_cuda or block_table.device != len_dev.device:
+            raise ValueError("len_dev and block_table must be CUDA tensors on one device")
+        if not len_dev.is_contiguous() or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+            raise ValueError("len_dev and the rows of block_table must be contiguous")
+        self.len_dev, self.block_table, self.device = len_dev, block_table, len_dev.device
+        self.batch, self.max_pages = (int(x) for x in block_table.shape)
+        stride = int(block_table.stride(0)) if self.batch > 1 else self.max_pages
+        self.struct = _PagedBatchStruct(self.batch, self.max_pages, stride, len_dev.data_ptr(), block_table.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+
+class Rope:
+    """A rotation table [max_positions, rotary_dim] float32 on the device (tq_make_rope_table's layout); ``interleaved``
+    turns adjacent channels instead of the two halves."""
+
+    def __init__(self, table: torch.Tensor, interleaved: bool = False):
+        if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous() or not table.is_cuda:
+            raise ValueError("table must be a contiguous CUDA float32 tensor [max_positions, rotary_dim]")
+        self.table, self.device = table, table.device
+        self.struct = _RopeStruct(int(table.shape[1]), int(table.shape[0]), int(bool(interleaved)), table.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+
+def _same_device(cache: PagedCache, batch: PagedBatch) -> None:
+    if batch.device != cache.device:
+        raise ValueError(f"the batch's tensors must be on the cache's device {cache.device}, got {batch.device}")
+
+
+def tq_paged_append(cache: PagedCache, batch: PagedBatch, cu_new: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                    q: torch.Tensor | None = None, rope: Rope | None = None, q_out: torch.Tensor | None = None,
+                    k_out: torch.Tensor | None = None, stream=None) -> None:
+    """Rotate and store new tokens: k, v [T, H_kv, d] and optionally q [T, H_q, d] (fp32, bf16 or fp16; tokens may lie
+    further apart than their rows), cu_new [B + 1] int32; rotated rows to q_out and k_out where given."""
+    dev, d = cache.device, cache.d
+    _same_device(cache, batch)
+    if k.dtype not in _PAGED_DTYPES:
+        raise TypeError(f"unsupported dtype {k.dtype}")
+    T = int(k.shape[0])
+    ks = _token_rows("k", k, cache.h_kv, d, k.dtype, dev)
+    vs = _token_rows("v", v, cache.h_kv, d, k.dtype, dev, T)
+    kos = _token_rows("k_out", k_out, cache.h_kv, d, k.dtype, dev, T) if k_out is not None else 0
+    qs = qos = hq = 0
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q needs q_out")
+        qs = _token_rows("q", q, None, d, k.dtype, dev, T)
+        hq = int(q.shape[1])
+        qos = _token_rows("q_out", q_out, hq, d, k.dtype, dev, T)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    if rope is not None and rope.device != dev:
+        raise ValueError(f"the rotation table must be on {dev}, got {rope.device}")
+    cu = _int32("cu_new", cu_new, batch.batch + 1, dev)
+    st = _on(dev, stream, lambda s: load().tq_paged_append(
+        cache.ref, batch.ref, rope.ref if rope is not None else None, cu, q.data_ptr() if q is not None else None,
+        k.data_ptr(), v.data_ptr(), _PAGED_DTYPES[k.dtype], hq, T, qs, ks, vs, q_out.data_ptr() if q is not None else None,
+        k_out.data_ptr() if k_out is not None else None, qos, kos, s))
+    _check("tq_paged_append", st)
+
+
+def tq_paged_gather(cache: PagedCache, batch: PagedBatch, cu_rows: torch.Tensor, k_out: torch.Tensor, v_out: torch.Tensor,
+                    first: torch.Tensor | None = None, stream=None) -> None:
+    """Cached tokens as rows of k_out, v_out [rows, H_kv, d] (fp32, bf16 or fp16): rows cu_rows[b] .. cu_rows[b + 1] - 1
+    get sequence b's tokens from position first[b] (0 where first is None)."""
+    dev, d = cache.device, cache.d
+    _same_device(cache, batch)
+    if k_out.dtype not in _PAGED_DTYPES:
+        raise TypeError(f"unsupported dtype {k_out.dtype}")
+    rows = int(k_out.shape[0])
+    ks = _token_rows("k_out", k_out, cache.h_kv, d, k_out.dtype, dev)
+    vs = _token_rows("v_out", v_out, cache.h_kv, d, k_out.dtype, dev, rows)
+    cu = _int32("cu_rows", cu_rows, batch.batch + 1, dev)
+    at = _int32("first", first, batch.batch, dev) if first is not None else None
+    st = _on(dev, stream, lambda s: load().tq_paged_gather(cache.ref, batch.ref, cu, at, rows, k_out.data_ptr(),
+                                                           v_out.data_ptr(), _PAGED_DTYPES[k_out.dtype], ks, vs, s))
+    _check("tq_paged_gather", st)
+
+
+def tq_paged_decode_workspace_size(cache: PagedCache, batch: int, h_q: int) -> int:
+    return _on(cache.device, 0, lambda _: int(load().tq_paged_decode_workspace_size(cache.ref, batch, h_q)))
+
+
+def paged_workspace_for(cache: PagedCache, batch: PagedBatch, h_q: int) -> torch.Tensor:
+    n = tq_paged_decode_workspace_size(cache, batch.batch, h_q)
+    if n == 0:
+        raise TQError("tq_paged_decode_workspace_size", 1)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def tq_paged_decode_attention(cache: PagedCache, batch: PagedBatch, q: torch.Tensor, out: torch.Tensor,
+                              workspace: torch.Tensor, softmax_scale: float | None = None, stream=None) -> None:
+    """Decode attention over the paged 4-bit cache: q, out [B, H_q, d] (bf16 or fp16), workspace a uint8 device tensor
+    (paged_workspace_for) that no other call in flight uses."""
+    dev, d = cache.device, cache.d
+    _same_device(cache, batch)
+    if q.dtype not in _HALF_DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    qs = _token_rows("q", q, None, d, q.dtype, dev, batch.batch)
+    hq = int(q.shape[1])
+    os_ = _token_rows("out", out, hq, d, q.dtype, dev, batch.batch)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
+    scale = (1.0 / d ** 0.5) if softmax_scale is None else float(softmax_scale)
+    st = _on(dev, stream, lambda s: load().tq_paged_decode_attention(
+        cache.ref, batch.ref, q.data_ptr(), _HALF_DTYPES[q.dtype], hq, qs, scale, out.data_ptr(), os_, workspace.data_ptr(),
+        workspace.numel(), s))
+    _check("tq_paged_decode_attention", st)
+
+
+def tq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+                        out: torch.Tensor, softmax_scale: float | None = None, stream=None) -> None:
+    """Causal attention of packed sequences: q, out [T_q, H_q, d], k, v [T_k, H_kv, d] (bf16 or fp16; tokens may lie
+    further apart than their rows), cu_q, cu_k [B + 1] int32.  Query i of a sequence sees keys j <= i + n_k - n_q."""
+    dev, dt = q.device, q.dtype
+    if dt not in _HALF_DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    if not q.is_cuda or q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be CUDA tensors [tokens, heads, d]")
+    d, hq, hkv = int(q.shape[2]), int(q.shape[1]), int(k.shape[1])
+    qs = _token_rows("q", q, hq, d, dt, dev)
+    os_ = _token_rows("out", out, hq, d, dt, dev, int(q.shape[0]))
+    ks = _token_rows("k", k, hkv, d, dt, dev)
+    vs = _token_rows("v", v, hkv, d, dt, dev, int(k.shape[0]))
+    if cu_q.dim() != 1 or cu_q.shape[0] < 2:
+        raise ValueError("cu_q must be [B + 1] with B >= 1")
+    B = int(cu_q.shape[0]) - 1
+    scale = (1.0 / d ** 0.5) if softmax_scale is None else float(softmax_scale)
+    cq, ck = _int32("cu_q", cu_q, B + 1, dev), _int32("cu_k", cu_k, B + 1, dev)
+    st = _on(dev, stream, lambda s: load().tq_prompt_attention(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), _HALF_DTYPES[dt], int(q.shape[0]), int(k.shape[0]), hq, hkv, d, qs, ks, vs,
+        cq, ck, B, scale, out.data_ptr(), os_, s))
+    _check("tq_prompt_attention", st)

@@ -20,10 +20,12 @@ Plain, slow, float64 NumPy written from the pages' statement of the method:
   over the compressed cache, explicit dequantization, and the brute-force
   softmax over dequantized K/V.
 * ``accounting`` -- storage bytes and compression ratios.
+* ``paged``     -- the paged 4-bit cache's layout, the position rotation and
+  softmax attention over given or cached K and V.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test
 against closed forms, textbook constants, the pages' printed numbers or
 brute force (see tests/test_oracle_*.py).  No function is "parity unpinned".
 """
 
-from . import accounting, attention, codebook, layout, quant  # noqa: F401
+from . import accounting, attention, codebook, layout, paged, quant  # noqa: F401
