@@ -83,7 +83,7 @@ __device__ __forceinline__ int unit_sequence(const int32_t *cu, int batch, int r
     const int step = (n + 31) >> 5;
     const int at = lane * step;
     const bool below = at < n && (clamp_cu(cu, lo + at, rows) >> 4) + 2 * (lo + at) <= u;
-    const int k = __popc(__ballot_sync(0xffffffffu, below)) - 1;  // lane 0 always holds
+    const int k = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0);
     lo += k * step;
     n = min(step, n - k * step);
   }
@@ -176,10 +176,11 @@ struct PromptArgs {
   long long q_stride, k_stride, v_stride, out_stride;
   const int32_t *cu_q, *cu_k;
   int T_q, T_k, h_q, h_kv, batch;
-  float scale_log2;
+  float scale_log2;  // |softmax scale| times log2(e), at least 1e-30
+  int negate;        // the scale is negative
   unsigned long long wait_ns;
   unsigned int *errors;
 };
-cudaError_t launch_prompt(const PromptArgs &a, int d, tq_dtype dt, int num_sms, cudaStream_t stream);
+cudaError_t launch_prompt(const PromptArgs &a, int d, tq_dtype dt, cudaStream_t stream);
 
 }  // namespace tq

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       __syncwarp();
       issue();
       const int s = used % kStages;
-      if (!mbar_wait(&bars[s], (used / kStages) & 1, wait_ns)) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], (used / kStages) & 1, wait_ns))) {
         dead = true;
         if (lane == 0) atomicOr(a.c.errors, TQ_ERRF_DECODE_WAIT);
         break;
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
   }
   // a warp that gave up still waits for its own copies
   if (dead)
-    for (int i = used; i < asked; ++i) mbar_wait(&bars[i % kStages], (i / kStages) & 1, wait_ns);
+    for (int i = used; i < asked; ++i) mbar_wait(&bars[i % kStages], (i / kStages) & 1);
 }
 
 // Joins the parts of each unit that more than one range holds; zeros for

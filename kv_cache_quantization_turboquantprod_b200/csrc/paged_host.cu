@@ -198,11 +198,13 @@ tq_status tq_prompt_attention(const void *q, const void *k, const void *v, tq_dt
   a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride; a.out_stride = out_stride;
   a.cu_q = cu_q; a.cu_k = cu_k;
   a.T_q = T_q; a.T_k = T_k; a.h_q = h_q; a.h_kv = h_kv; a.batch = batch;
-  a.scale_log2 = softmax_scale * kLog2e;
+  // a scale of 0 becomes one that leaves every weight at 1 (masked scores
+  // are infinite, and 0 times infinity is NaN)
+  a.scale_log2 = std::fmax(std::fabs(softmax_scale) * kLog2e, 1e-30f);
+  a.negate = softmax_scale < 0.f;
   a.wait_ns = tq::wait_limit_ns();
-  int sms = 0;
-  if (tq::device_sm_count(&sms) != cudaSuccess || tq::device_error_word(&a.errors) != cudaSuccess) return TQ_ERR_CUDA;
-  return done(tq::launch_prompt(a, d, dtype, sms, (cudaStream_t)stream));
+  if (tq::device_error_word(&a.errors) != cudaSuccess) return TQ_ERR_CUDA;
+  return done(tq::launch_prompt(a, d, dtype, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -169,6 +169,15 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int c0,
       : "memory");
 }
 
+// The same of a 3-D tensor map.
+__device__ __forceinline__ void tma_load_3d(void *dst, const void *tmap, int c0, int c1, int c2, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+      "[%5];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Make generic-proxy shared-memory writes visible to the async proxy
 // (tensor core operand reads).
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -347,6 +356,16 @@ __device__ __forceinline__ uint64_t smem_desc(const void *base, uint32_t lbo, ui
   return d;
 }
 
+// Shared-memory matrix descriptor with the 128-byte swizzle (what a tensor
+// map of 128-byte boxes writes), 1024-byte aligned atoms of 8 rows.  K-major:
+// sbo = stride of 8-row groups, lbo unused.  MN-major: lbo = stride of
+// 64-element (16-bit) blocks along M or N, sbo = stride of 8-row groups
+// along K.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 | (uint64_t)((sbo >> 4) & 0x3FFF) << 32 |
+         1ull << 46 | 2ull << 61;
+}
+
 // Instruction descriptor of tcgen05.mma kind::i8: s32 accumulate.
 // a_signed / b_signed: operand signedness; a_mn / b_mn: 1 = MN-major.
 __host__ __device__ constexpr uint32_t idesc_i8(int M, int N, bool a_signed, bool b_signed,
@@ -388,6 +407,10 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool a_mn, bool b
   return (1u << 4)                          // c format: f32 (a, b format 0: f16)
          | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// The same with both operands bf16 or both fp16, and A negated or not.
+__host__ __device__ constexpr uint32_t idesc_16bit(int M, int N, bool bf16, bool b_mn, bool negate_a) {
+  return idesc_f16(M, N, false, b_mn) | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (negate_a ? 1u << 13 : 0u);
 }
 // D[tmem] (+)= A[smem desc] * B[smem desc], kind::f16
 __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
