@@ -617,7 +617,9 @@ cudaError_t launch(const PagedDecodeArgs &a, cudaStream_t stream) {
   const int G = a.h_q / a.c.h_kv, blocks = a.num_sms * blocks_per_sm(D);
   const size_t smem = Smem<D>::bytes(G);
   auto *kernel = paged_decode_kernel<D, T>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (always for the widest group, so that no order of calls lowers it)
+  static std::atomic<int> allowed[kAttributeDevices];
+  cudaError_t e = allow_smem(kernel, Smem<D>::bytes(TQ_PAGED_MAX_GQA), allowed);
   if (e != cudaSuccess) return e;
   kernel<<<blocks, kThreads, smem, stream>>>(a, wait_limit_ns());
   e = cudaGetLastError();

@@ -38,6 +38,7 @@
 #include "paged.cuh"
 #include "sm100.cuh"
 #include "tq_common.cuh"
+#include "tq_kernels.h"
 
 namespace tq {
 namespace {
@@ -438,7 +439,8 @@ cudaError_t launch(const PromptArgs &a, cudaStream_t stream) {
       !encode<D, T>(&v, none ? a.q : a.v, none ? a.q_stride : a.v_stride, none ? a.h_q : a.h_kv, 0, none ? a.T_q : a.T_k, C::kKeys))
     return cudaErrorInvalidValue;
   auto *kernel = prompt_kernel<D, T>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  static std::atomic<int> allowed[kAttributeDevices];
+  const cudaError_t e = allow_smem(kernel, C::kSmem, allowed);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)(units * a.h_kv), C::kThreads, C::kSmem, stream>>>(a, q, k, v, (int)units);
   return cudaGetLastError();

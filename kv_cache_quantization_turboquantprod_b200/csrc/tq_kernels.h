@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <utility>
 
 #include "tq.h"
@@ -29,6 +30,21 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// Let `kernel` use `bytes` of dynamic shared memory, set once per kernel and
+// device (the largest value wins; `done` is the caller's own static array).
+constexpr int kAttributeDevices = 64;
+template <typename Kernel>
+cudaError_t allow_smem(Kernel *kernel, size_t bytes, std::atomic<int> (&done)[kAttributeDevices]) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool kept = dev >= 0 && dev < kAttributeDevices;
+  if (kept && done[dev].load(std::memory_order_relaxed) >= (int)bytes) return cudaSuccess;
+  const cudaError_t s = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (s == cudaSuccess && kept) done[dev].store((int)bytes, std::memory_order_relaxed);
+  return s;
 }
 
 // Arguments of one quantize_append launch.  Passed by value as a

@@ -491,35 +491,41 @@ _PAGED_DTYPES = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: 
 _HALF_DTYPES = {torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
 
 
-def _token_rows(name: str, t: torch.Tensor, heads: int | None, d: int, dtype, device, rows: int | None = None) -> int:
+def _token_rows(name: str, t: torch.Tensor, heads: int, d: int, dtype, device, rows: int) -> int:
     """Check [rows, heads, d] token rows whose heads are contiguous (tokens may lie further apart); returns the tokens'
     stride in elements."""
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or t.shape[2] != d or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'tokens' if rows is None else rows}, {'heads' if heads is None else heads}, {d}], "
-                         f"got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.shape != (rows, heads, d):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {tuple(t.shape)}")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     stride, by_head, by_channel = t.stride()
-    h = t.shape[1]
-    if by_channel != 1 or (by_head != d and h > 1):
+    if by_channel != 1 or (by_head != d and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous rows")
-    return stride if t.shape[0] > 1 else max(stride, h * d)
+    return stride if rows > 1 else max(stride, heads * d)
+
+
+def _three_dims(name: str, t: torch.Tensor):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, d], got {tuple(t.shape)}")
+    return t.shape
 
 
 def _int32(name: str, t: torch.Tensor, n: int, device) -> int:
-    if t.dtype != torch.int32 or tuple(t.shape) != (n,) or t.device != device or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != (n,) or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor [{n}] on {device}")
     return t.data_ptr()
 
 
-def _on(device, stream, call):
-    """call(stream handle) with `device` current: its kernels run there whatever device the caller has selected."""
-    if torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
+def _call(fn, device, stream, *args) -> int:
+    """fn(*args, stream handle) with `device` current: its kernels run there whatever device the caller has selected, on the
+    device's current stream where none is given."""
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
     with torch.cuda.device(device):
-        return call(torch.cuda.current_stream(device).cuda_stream if stream is None else _stream(stream))
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream))
 
 
 def tq_make_rope_table(max_positions: int, rotary_dim: int, theta: float = 10000.0) -> torch.Tensor:
@@ -592,30 +598,30 @@ def tq_paged_append(cache: PagedCache, batch: PagedBatch, cu_new: torch.Tensor, 
                     k_out: torch.Tensor | None = None, stream=None) -> None:
     """Rotate and store new tokens: k, v [T, H_kv, d] and optionally q [T, H_q, d] (fp32, bf16 or fp16; tokens may lie
     further apart than their rows), cu_new [B + 1] int32; rotated rows to q_out and k_out where given."""
-    dev, d = cache.device, cache.d
+    dev, d, dt = cache.device, cache.d, k.dtype
     _same_device(cache, batch)
-    if k.dtype not in _PAGED_DTYPES:
-        raise TypeError(f"unsupported dtype {k.dtype}")
-    T = int(k.shape[0])
-    ks = _token_rows("k", k, cache.h_kv, d, k.dtype, dev)
-    vs = _token_rows("v", v, cache.h_kv, d, k.dtype, dev, T)
-    kos = _token_rows("k_out", k_out, cache.h_kv, d, k.dtype, dev, T) if k_out is not None else 0
+    if dt not in _PAGED_DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    T = k.shape[0]
+    ks = _token_rows("k", k, cache.h_kv, d, dt, dev, T)
+    vs = _token_rows("v", v, cache.h_kv, d, dt, dev, T)
+    kos, kp = (_token_rows("k_out", k_out, cache.h_kv, d, dt, dev, T), k_out.data_ptr()) if k_out is not None else (0, None)
     qs = qos = hq = 0
+    qp = qop = None
     if q is not None:
         if q_out is None:
             raise ValueError("q needs q_out")
-        qs = _token_rows("q", q, None, d, k.dtype, dev, T)
-        hq = int(q.shape[1])
-        qos = _token_rows("q_out", q_out, hq, d, k.dtype, dev, T)
+        hq = _three_dims("q", q)[1]
+        qs = _token_rows("q", q, hq, d, dt, dev, T)
+        qos = _token_rows("q_out", q_out, hq, d, dt, dev, T)
+        qp, qop = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if rope is not None and rope.device != dev:
         raise ValueError(f"the rotation table must be on {dev}, got {rope.device}")
     cu = _int32("cu_new", cu_new, batch.batch + 1, dev)
-    st = _on(dev, stream, lambda s: load().tq_paged_append(
-        cache.ref, batch.ref, rope.ref if rope is not None else None, cu, q.data_ptr() if q is not None else None,
-        k.data_ptr(), v.data_ptr(), _PAGED_DTYPES[k.dtype], hq, T, qs, ks, vs, q_out.data_ptr() if q is not None else None,
-        k_out.data_ptr() if k_out is not None else None, qos, kos, s))
+    st = _call(load().tq_paged_append, dev, stream, cache.ref, batch.ref, rope.ref if rope is not None else None, cu, qp,
+               k.data_ptr(), v.data_ptr(), _PAGED_DTYPES[dt], hq, T, qs, ks, vs, qop, kp, qos, kos)
     _check("tq_paged_append", st)
 
 
@@ -623,22 +629,23 @@ def tq_paged_gather(cache: PagedCache, batch: PagedBatch, cu_rows: torch.Tensor,
                     first: torch.Tensor | None = None, stream=None) -> None:
     """Cached tokens as rows of k_out, v_out [rows, H_kv, d] (fp32, bf16 or fp16): rows cu_rows[b] .. cu_rows[b + 1] - 1
     get sequence b's tokens from position first[b] (0 where first is None)."""
-    dev, d = cache.device, cache.d
+    dev, d, dt = cache.device, cache.d, k_out.dtype
     _same_device(cache, batch)
-    if k_out.dtype not in _PAGED_DTYPES:
-        raise TypeError(f"unsupported dtype {k_out.dtype}")
-    rows = int(k_out.shape[0])
-    ks = _token_rows("k_out", k_out, cache.h_kv, d, k_out.dtype, dev)
-    vs = _token_rows("v_out", v_out, cache.h_kv, d, k_out.dtype, dev, rows)
+    if dt not in _PAGED_DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    rows = k_out.shape[0]
+    ks = _token_rows("k_out", k_out, cache.h_kv, d, dt, dev, rows)
+    vs = _token_rows("v_out", v_out, cache.h_kv, d, dt, dev, rows)
     cu = _int32("cu_rows", cu_rows, batch.batch + 1, dev)
     at = _int32("first", first, batch.batch, dev) if first is not None else None
-    st = _on(dev, stream, lambda s: load().tq_paged_gather(cache.ref, batch.ref, cu, at, rows, k_out.data_ptr(),
-                                                           v_out.data_ptr(), _PAGED_DTYPES[k_out.dtype], ks, vs, s))
+    st = _call(load().tq_paged_gather, dev, stream, cache.ref, batch.ref, cu, at, rows, k_out.data_ptr(), v_out.data_ptr(),
+               _PAGED_DTYPES[dt], ks, vs)
     _check("tq_paged_gather", st)
 
 
 def tq_paged_decode_workspace_size(cache: PagedCache, batch: int, h_q: int) -> int:
-    return _on(cache.device, 0, lambda _: int(load().tq_paged_decode_workspace_size(cache.ref, batch, h_q)))
+    with torch.cuda.device(cache.device):
+        return int(load().tq_paged_decode_workspace_size(cache.ref, batch, h_q))
 
 
 def paged_workspace_for(cache: PagedCache, batch: PagedBatch, h_q: int) -> torch.Tensor:
@@ -652,19 +659,18 @@ def tq_paged_decode_attention(cache: PagedCache, batch: PagedBatch, q: torch.Ten
                               workspace: torch.Tensor, softmax_scale: float | None = None, stream=None) -> None:
     """Decode attention over the paged 4-bit cache: q, out [B, H_q, d] (bf16 or fp16), workspace a uint8 device tensor
     (paged_workspace_for) that no other call in flight uses."""
-    dev, d = cache.device, cache.d
+    dev, d, dt = cache.device, cache.d, q.dtype
     _same_device(cache, batch)
-    if q.dtype not in _HALF_DTYPES:
-        raise TypeError(f"unsupported dtype {q.dtype}")
-    qs = _token_rows("q", q, None, d, q.dtype, dev, batch.batch)
-    hq = int(q.shape[1])
-    os_ = _token_rows("out", out, hq, d, q.dtype, dev, batch.batch)
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+    if dt not in _HALF_DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    hq = _three_dims("q", q)[1]
+    qs = _token_rows("q", q, hq, d, dt, dev, batch.batch)
+    os_ = _token_rows("out", out, hq, d, dt, dev, batch.batch)
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
     scale = (1.0 / d ** 0.5) if softmax_scale is None else float(softmax_scale)
-    st = _on(dev, stream, lambda s: load().tq_paged_decode_attention(
-        cache.ref, batch.ref, q.data_ptr(), _HALF_DTYPES[q.dtype], hq, qs, scale, out.data_ptr(), os_, workspace.data_ptr(),
-        workspace.numel(), s))
+    st = _call(load().tq_paged_decode_attention, dev, stream, cache.ref, batch.ref, q.data_ptr(), _HALF_DTYPES[dt], hq, qs,
+               scale, out.data_ptr(), os_, workspace.data_ptr(), workspace.numel())
     _check("tq_paged_decode_attention", st)
 
 
@@ -675,19 +681,19 @@ def tq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q:
     dev, dt = q.device, q.dtype
     if dt not in _HALF_DTYPES:
         raise TypeError(f"unsupported dtype {dt}")
-    if not q.is_cuda or q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q and k must be CUDA tensors [tokens, heads, d]")
-    d, hq, hkv = int(q.shape[2]), int(q.shape[1]), int(k.shape[1])
-    qs = _token_rows("q", q, hq, d, dt, dev)
-    os_ = _token_rows("out", out, hq, d, dt, dev, int(q.shape[0]))
-    ks = _token_rows("k", k, hkv, d, dt, dev)
-    vs = _token_rows("v", v, hkv, d, dt, dev, int(k.shape[0]))
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    Tq, hq, d = _three_dims("q", q)
+    Tk, hkv, _ = _three_dims("k", k)
+    qs = _token_rows("q", q, hq, d, dt, dev, Tq)
+    os_ = _token_rows("out", out, hq, d, dt, dev, Tq)
+    ks = _token_rows("k", k, hkv, d, dt, dev, Tk)
+    vs = _token_rows("v", v, hkv, d, dt, dev, Tk)
     if cu_q.dim() != 1 or cu_q.shape[0] < 2:
         raise ValueError("cu_q must be [B + 1] with B >= 1")
-    B = int(cu_q.shape[0]) - 1
+    B = cu_q.shape[0] - 1
     scale = (1.0 / d ** 0.5) if softmax_scale is None else float(softmax_scale)
-    cq, ck = _int32("cu_q", cu_q, B + 1, dev), _int32("cu_k", cu_k, B + 1, dev)
-    st = _on(dev, stream, lambda s: load().tq_prompt_attention(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), _HALF_DTYPES[dt], int(q.shape[0]), int(k.shape[0]), hq, hkv, d, qs, ks, vs,
-        cq, ck, B, scale, out.data_ptr(), os_, s))
+    st = _call(load().tq_prompt_attention, dev, stream, q.data_ptr(), k.data_ptr(), v.data_ptr(), _HALF_DTYPES[dt], Tq, Tk, hq,
+               hkv, d, qs, ks, vs, _int32("cu_q", cu_q, B + 1, dev), _int32("cu_k", cu_k, B + 1, dev), B, scale, out.data_ptr(),
+               os_)
     _check("tq_prompt_attention", st)
