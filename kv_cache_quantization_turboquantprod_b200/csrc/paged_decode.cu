@@ -25,17 +25,21 @@
 //    queries), one f32 accumulator per group of 32 channels; then
 //    x = sum_j scale_j acc_j + sum_j zero_j qsum_j, the second sum as one
 //    more product with the group sums of q in two fp16 parts.
-//  * values: A = codes of 16 channels x 16 tokens, B = p scale_j, f32
-//    accumulators; sum p zero_j in f32 beside it.  fp16 outputs take p scale_j
-//    in two fp16 parts (22 bits), bf16 outputs in one (2^-12 against the
-//    output's own 2^-9).
-// mma.sync carries them: 17 products of 16 x 8 x 16 a cell keep its tensor
+//  * values: A = codes of 16 channels x 16 tokens, B = p scale_j of 16 tokens
+//    x 8 heads (p's fragment transposed by movmatrix).  One more product gives
+//    sum p zero_j (A = zeros, a group a row) and sum p (A = ones, row 8).
+//    bf16 outputs take p and p scale_j in fp16 (2^-12 each against the
+//    output's own 2^-9); fp16 outputs take both in two fp16 parts (22 bits).
+// mma.sync carries them: 18 products of 16 x 8 x 16 a cell keep its tensor
 // pipe busy a third of the time that the bytes take, and the operands come
-// from registers without a trip through tensor memory.
+// from registers without a trip through tensor memory.  (Queries as A with
+// idle rows 8..15 need no transposition, but their zero registers cost 60
+// moves a cell.)
 //
 // Softmax.  Weights are 2^(x - M) with a running reference M per head that
-// only has to keep p scale_j below 2^14; it moves (and the accumulators with
-// it) when a token exceeds it by 2^4, which one vote per cell finds out.
+// only has to keep p and p scale_j in fp16's range, and a bound E of the value
+// scales' exponents; both move (and the accumulators with them) when a token
+// exceeds them, which one vote a step (two cells) finds out.
 #include "paged.cuh"
 #include "sm100.cuh"
 #include "tq_common.cuh"
@@ -47,14 +51,16 @@ namespace {
 using namespace sm100;
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kStages = 3;
-constexpr float kTop = 10.f, kSlack = 4.f;  // p scale <= 2^10 when M moves, < 2^14 always
+constexpr int kStep = 2;    // cells of a step
+constexpr int kStages = 2;  // steps in a warp's ring
+constexpr float kTop = 10.f, kSlack = 4.f;  // p 2^E <= 2^10 when M moves, < 2^14 always
 
 __host__ __device__ constexpr int blocks_per_sm(int d) { return d == 256 ? 1 : 2; }
 
 template <int D>
 struct Smem {
-  static constexpr int kRing = kWarps * kStages * Cell<D>::kBytes;
+  static constexpr int kStage = kStep * Cell<D>::kBytes;
+  static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kBars = kRing;                            // [kWarps][kStages] u64
   static constexpr int kScan = kBars + kWarps * kStages * 8;     // 16 long long
   static constexpr int kState = kScan + 128;                     // [kWarps][8][2] floats: M, l
@@ -62,12 +68,20 @@ struct Smem {
   static constexpr size_t bytes(int G) { return kMerge + (size_t)kWarps * G * D * 4; }
 };
 
+// c += a b, and d = a b, for m16n8k16 fp16 operands.
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                       uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                           uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -76,6 +90,22 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) { return pack2<__half>(a, b); }
 __device__ __forceinline__ float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The P words of a lane.
+template <int P>
+__device__ __forceinline__ void load_words(uint32_t (&w)[P], const uint8_t *p) {
+  if constexpr (P == 4) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    w[0] = u.x; w[1] = u.y;
+  }
+}
 
 // Cells of a sequence; lengths beyond the table's row count as that row.
 __device__ __forceinline__ int cells_of(const PagedView &c, int b) {
@@ -89,13 +119,16 @@ __device__ __forceinline__ long long warp_sum_ll(long long x) {
   return x;
 }
 
-// Cells before sequence `upto` and of the whole batch, times h_kv.  All
+// Steps of a sequence: two cells each, the last one perhaps one.
+__device__ __forceinline__ int steps_of(const PagedView &c, int b) { return (cells_of(c, b) + kStep - 1) / kStep; }
+
+// Steps before sequence `upto` and of the whole batch, times h_kv.  All
 // threads of the block (at most 256) call; scratch: 16 long long.
-__device__ __forceinline__ void sum_cells(const PagedView &c, int upto, long long *scratch, long long *before,
+__device__ __forceinline__ void sum_steps(const PagedView &c, int upto, long long *scratch, long long *before,
                                           long long *total) {
   long long s = 0, t = 0;
   for (int b = threadIdx.x; b < c.batch; b += blockDim.x) {
-    const int n = cells_of(c, b);
+    const int n = steps_of(c, b);
     t += n;
     if (b < upto) s += n;
   }
@@ -117,27 +150,27 @@ __device__ __forceinline__ void sum_cells(const PagedView &c, int upto, long lon
   *total = t * c.h_kv;
 }
 
-// Cells of a block's range: an equal share, at least one per warp.
-__host__ __device__ __forceinline__ long long range_cells(long long total, int blocks) {
+// Steps of a block's range: an equal share, at least one per warp.
+__host__ __device__ __forceinline__ long long range_steps(long long total, int blocks) {
   const long long per = (total + blocks - 1) / blocks;
   return per < kWarps ? kWarps : per;
 }
 
-// A place in the order (sequence, KV head, cell).
+// A place in the order (sequence, KV head, step).
 struct Cursor {
-  int b, h, cell, cells;
+  int b, h, step, steps;
   __device__ __forceinline__ void settle(const PagedView &c) {
-    while (cell >= cells) {
-      cell -= cells;
+    while (step >= steps) {
+      step -= steps;
       if (++h == c.h_kv) {
         h = 0;
         do {
           if (++b >= c.batch) {  // past the end: never used
-            cells = 0x7fffffff;
+            steps = 0x7fffffff;
             return;
           }
-          cells = cells_of(c, b);
-        } while (cells == 0);
+          steps = steps_of(c, b);
+        } while (steps == 0);
       }
     }
   }
@@ -154,7 +187,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int G = a.h_q / a.c.h_kv;
-  uint8_t *const ring = smem + warp * kStages * C::kBytes;
+  uint8_t *const ring = smem + warp * kStages * S::kStage;
   uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + S::kBars) + warp * kStages;
   long long *const scan = reinterpret_cast<long long *>(smem + S::kScan);
   float *const state = reinterpret_cast<float *>(smem + S::kState);
@@ -167,9 +200,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
   }
   // ---- this block's range, and the sequence it starts in
   long long total, unused;
-  sum_cells(a.c, 0, scan, &unused, &total);
+  sum_steps(a.c, 0, scan, &unused, &total);
   pdl_trigger();
-  const long long per = range_cells(total, gridDim.x);
+  const long long per = range_steps(total, gridDim.x);
   const long long c0 = per * blockIdx.x;
   if (c0 >= total) return;
   const int count = (int)(min(c0 + per, total) - c0);
@@ -177,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     long long base = 0;
     for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
       const int b = b0 + tid;
-      const long long n = b < a.c.batch ? (long long)cells_of(a.c, b) * a.c.h_kv : 0;
+      const long long n = b < a.c.batch ? (long long)steps_of(a.c, b) * a.c.h_kv : 0;
       long long inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -201,59 +234,87 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     }
     __syncthreads();
   }
-  Cursor here;  // the range's first cell
+  Cursor here;  // the range's first step
   here.b = (int)scan[8];
-  here.cells = cells_of(a.c, here.b);
-  here.h = (int)((c0 - scan[9]) / here.cells);
-  here.cell = (int)((c0 - scan[9]) % here.cells);
+  here.steps = steps_of(a.c, here.b);
+  here.h = (int)((c0 - scan[9]) / here.steps);
+  here.step = (int)((c0 - scan[9]) % here.steps);
 
-  // ---- the warp's copies: cells warp, warp + kWarps, .. of the range
+  // ---- the warp's copies: steps warp, warp + kWarps, .. of the range.  The
+  // page of a step's cells (one page where pages hold two cells or more) is
+  // looked up a step before their copy.
   Cursor next = here;
-  next.cell += warp;
+  next.step += warp;
   next.settle(a.c);
   const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
-  int asked = 0;            // cells whose copy was issued
-  int page = mine > 0 ? page_of(a.c, next.b, next.cell * kCell) : -1;
-  uint32_t bad_stage = 0;   // stages whose cell has no page
-  auto issue = [&]() {      // copy of cell `asked`; then look up the next cell's page
+  const int per_page = a.c.page_shift - 4;  // log2 of the cells of a page
+  const uint32_t head_bytes = (uint32_t)C::kBytes << per_page;
+  const size_t page_bytes = (size_t)head_bytes * a.c.h_kv;
+  const bool joined = per_page > 0;
+  int cells = 0, page0 = 0, page1 = 0;
+  const int32_t *row = a.c.table;
+  auto enter = [&] {  // next.b changed
+    cells = cells_of(a.c, next.b);
+    row = a.c.table + (size_t)next.b * a.c.table_stride;
+  };
+  auto look = [&] {
+    page0 = row[(kStep * next.step) >> per_page];
+    if (!joined) page1 = kStep * next.step + 1 < cells ? row[kStep * next.step + 1] : 0;
+  };
+  int asked = 0;  // steps whose copies were issued
+  if (mine > 0) {
+    enter();
+    look();
+  }
+  uint32_t bad_stage = 0;  // stages with a cell that has no page
+  auto issue = [&] {       // copies of step `asked`; then look the next one up
     if (asked >= mine) return;
-    const int s = asked % kStages;
-    if (page >= 0) {
-      bad_stage &= ~(1u << s);
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&bars[s], C::kBytes);
-        bulk_g2s(ring + s * C::kBytes, cell_ptr<D>(a.c, page, next.cell * kCell, next.h), C::kBytes, &bars[s]);
+    const int s = asked % kStages, first = kStep * next.step, have = min(cells - first, kStep);
+    const bool bad = (uint32_t)page0 >= (uint32_t)a.c.num_pages || (!joined && (uint32_t)page1 >= (uint32_t)a.c.num_pages);
+    bad_stage = (bad_stage & ~(1u << s)) | ((uint32_t)bad << s);
+    if (lane == 0) {
+      uint8_t *const to = ring + s * S::kStage;
+      const uint8_t *const from = a.c.data + (size_t)page0 * page_bytes + (size_t)next.h * head_bytes;
+      if (bad) {
+        mbar_arrive(&bars[s]);
+      } else if (joined) {
+        mbar_arrive_expect_tx(&bars[s], have * C::kBytes);
+        bulk_g2s(to, from + (first & ((1 << per_page) - 1)) * C::kBytes, have * C::kBytes, &bars[s]);
+      } else {
+        mbar_arrive_expect_tx(&bars[s], have * C::kBytes);
+        bulk_g2s(to, from, C::kBytes, &bars[s]);
+        if (have > 1)
+          bulk_g2s(to + C::kBytes, a.c.data + (size_t)page1 * page_bytes + (size_t)next.h * head_bytes, C::kBytes, &bars[s]);
       }
-    } else {
-      bad_stage |= 1u << s;
-      if (lane == 0) mbar_arrive(&bars[s]);
     }
-    ++asked;
-    if (asked < mine) {
-      next.cell += kWarps;
-      next.settle(a.c);
-      page = page_of(a.c, next.b, next.cell * kCell);
+    if (++asked < mine) {
+      next.step += kWarps;
+      if (next.step >= next.steps) {
+        const int was = next.b;
+        next.settle(a.c);
+        if (next.b != was) enter();
+      }
+      look();
     }
   };
   __syncwarp();
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue();
+  issue();
 
-  int used = 0;             // cells taken
-  int at = 0;               // first cell of the current part, counted from the range's start
-  bool dead = false;        // a wait ran out
+  int used = 0;       // steps taken
+  int at = 0;         // first step of the current part, counted from the range's start
+  bool dead = false;  // a wait ran out
   const float kInf = INFINITY;
 
   while (at < count) {
-    // ---- one part: cells [at, end) of the range, all of unit (here.b, here.h)
-    const int end = min(count, at + here.cells - here.cell);
+    // ---- one part: steps [at, end) of the range, all of unit (here.b, here.h)
+    const int end = min(count, at + here.steps - here.step);
     const int len = a.c.len[here.b];
     bool bad = len > (a.c.max_pages << a.c.page_shift);
 
     // queries: head g of the unit, lane t's channels 32 j + 8 t .. + 7
-    uint32_t qb[NG][4];     // (0, 4), (2, 6) at weight 1; (1, 5), (3, 7) at 1/16
-    uint32_t qz[2];         // group sums of q, two fp16 parts, 2^-6
-    float c1[2], c2[2];     // heads 2 t, 2 t + 1: factors of the two score sums
+    uint32_t qb[NG][4];  // (0, 4), (2, 6) at weight 1; (1, 5), (3, 7) at 1/16
+    uint32_t qz[2];      // group sums of q, two fp16 parts, 2^-6
+    float c1[2];         // heads 2 t, 2 t + 1: from the products' scale to base-2 logits
     {
       float x[NG][8], big = 0.f;
       const T *q = reinterpret_cast<const T *>(a.q) + (size_t)here.b * a.q_stride + (size_t)(here.h * G + g) * D + 8 * t;
@@ -305,20 +366,19 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       const uint32_t ph = pack_half2(hi[0], hi[1]), pl = pack_half2(lo[0], lo[1]);
       qz[0] = NG == 8 ? ph : part == 0 ? ph : part == 1 ? pl : 0u;
       qz[1] = NG == 8 ? pl : 0u;
-      const int e0 = __shfl_sync(0xffffffffu, eq, 8 * t), e1 = __shfl_sync(0xffffffffu, eq, 8 * t + 4);
-      c1[0] = ldexpf(a.scale_log2, 24 - e0);
-      c1[1] = ldexpf(a.scale_log2, 24 - e1);
-      c2[0] = ldexpf(a.scale_log2, 6 - e0);
-      c2[1] = ldexpf(a.scale_log2, 6 - e1);
+      c1[0] = ldexpf(a.scale_log2, 24 - __shfl_sync(0xffffffffu, eq, 8 * t));
+      c1[1] = ldexpf(a.scale_log2, 24 - __shfl_sync(0xffffffffu, eq, 8 * t + 4));
     }
 
-    float acc[2 * NG][4], zs[NG][2], M[2] = {-kInf, -kInf}, l[2] = {0.f, 0.f};
+    // acc[2 j + i]: channels 32 j + 4 g + 2 i (rows g) and + 1 (rows g + 8), heads 2 t and 2 t + 1;
+    // zs: sum p zero of group g, heads 2 t and 2 t + 1, and sum p (lanes of g = 0); M: heads 2 t and 2 t + 1
+    float acc[2 * NG][4], zs[4] = {0.f, 0.f, 0.f, 0.f}, M[2] = {-kInf, -kInf};
+    int E = -1;
+    const uint32_t ones = g == 0 ? 0x3c003c00u : 0u;
 #pragma unroll
     for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) zs[j][0] = zs[j][1] = 0.f;
 
     for (int idx = used * kWarps + warp; idx < end && !dead; idx += kWarps, ++used) {
       __syncwarp();
@@ -333,186 +393,200 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
         bad = true;
         continue;
       }
-      uint8_t *const cell = ring + s * C::kBytes;
-      const int valid = len - (here.cell + idx - at) * kCell;
-      if (valid < kCell) {
+      uint8_t *const stage = ring + s * S::kStage;
+      const int valid = len - (here.step + idx - at) * (kStep * kCell);
+      if (valid < kStep * kCell) {
         // slots behind the sequence may hold anything: give them scale and zero 0
-        for (int i = lane; i < kCell * NG; i += 32) {
+        for (int i = lane; i < kStep * kCell * NG; i += 32) {
           const int n = i / NG, j = i % NG;
           if (n >= valid) {
-            *reinterpret_cast<uint16_t *>(cell + C::kKeyScale + C::scale_at(n, j)) = 0;
-            *reinterpret_cast<uint16_t *>(cell + C::kKeyZero + C::key_zero_at(n, j)) = 0;
-            *reinterpret_cast<uint16_t *>(cell + C::kValScale + C::scale_at(n, j)) = 0;
-            *reinterpret_cast<uint16_t *>(cell + C::kValZero + C::scale_at(n, j)) = 0;
+            uint8_t *const cell = stage + (n / kCell) * C::kBytes;
+            *reinterpret_cast<uint16_t *>(cell + C::kKeyScale + C::scale_at(n % kCell, j)) = 0;
+            *reinterpret_cast<uint16_t *>(cell + C::kKeyZero + C::key_zero_at(n % kCell, j)) = 0;
+            *reinterpret_cast<uint16_t *>(cell + C::kValScale + C::scale_at(n % kCell, j)) = 0;
+            *reinterpret_cast<uint16_t *>(cell + C::kValZero + C::scale_at(n % kCell, j)) = 0;
           }
         }
         fence_proxy_async_smem();  // before a later copy into this stage
         __syncwarp();
       }
 
-      // ---- scores of tokens g and g + 8 for heads 2 t and 2 t + 1
-      float x[4] = {0.f, 0.f, 0.f, 0.f};  // (g, 2t), (g, 2t+1), (g+8, 2t), (g+8, 2t+1)
-      const uint32_t pick = (g & 1) ? 0x7632 : 0x5410;  // halves e = g & 1 of a pair of words
+      // ---- scores (to be scaled by c1): x[.][0, 1] token g of a cell, heads 2 t and 2 t + 1; x[.][2, 3] token g + 8
+      float x[kStep][4];
+      const uint32_t pick = (g & 1) ? 0x7632 : 0x5410;  // halves e = g & 1 of two words
 #pragma unroll
-      for (int jp = 0; jp < NG / P; ++jp) {
-        uint32_t w0[P], w1[P];
-        const uint8_t *k0 = cell + C::key_word(g, jp * P, t), *k1 = cell + C::key_word(g + 8, jp * P, t);
-        if constexpr (P == 4) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(k0), v = *reinterpret_cast<const uint4 *>(k1);
-          w0[0] = u.x; w0[1] = u.y; w0[2] = u.z; w0[3] = u.w;
-          w1[0] = v.x; w1[1] = v.y; w1[2] = v.z; w1[3] = v.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2 *>(k0), v = *reinterpret_cast<const uint2 *>(k1);
-          w0[0] = u.x; w0[1] = u.y;
-          w1[0] = v.x; w1[1] = v.y;
-        }
+      for (int ce = 0; ce < kStep; ++ce) {
+        const uint8_t *const cell = stage + ce * C::kBytes;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < P; i += 2) {
-          // scales of groups j, j + 1: words (s, e) -> tokens g, g + 8
-          const uint4 sw = *reinterpret_cast<const uint4 *>(cell + C::kKeyScale + C::scale_at(g & 7, jp * P + i) - 2 * (g & 1));
-          const uint32_t pair[2] = {__byte_perm(sw.x, sw.y, pick), __byte_perm(sw.z, sw.w, pick)};
+        for (int jp = 0; jp < NG / P; ++jp) {
+          uint32_t w0[P], w1[P];
+          load_words(w0, cell + C::key_word(g, jp * P, t));
+          load_words(w1, cell + C::key_word(g + 8, jp * P, t));
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int j = jp * P + i + k;
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            const uint32_t u = w0[i + k], v = w1[i + k], us = u >> 8, vs = v >> 8;
-            mma16(d, u & 0x000f000fu, v & 0x000f000fu, us & 0x000f000fu, vs & 0x000f000fu, qb[j][0], qb[j][1]);
-            mma16(d, u & 0x00f000f0u, v & 0x00f000f0u, us & 0x00f000f0u, vs & 0x00f000f0u, qb[j][2], qb[j][3]);
-            const float2 sc = unpack_half2(pair[k]);
-            x[0] = fmaf(sc.x, d[0], x[0]);
-            x[1] = fmaf(sc.x, d[1], x[1]);
-            x[2] = fmaf(sc.y, d[2], x[2]);
-            x[3] = fmaf(sc.y, d[3], x[3]);
+          for (int i = 0; i < P; i += 2) {
+            const uint4 sw = *reinterpret_cast<const uint4 *>(cell + C::kKeyScale + C::scale_at(g & 6, jp * P + i));
+            const uint32_t pair[2] = {__byte_perm(sw.x, sw.y, pick), __byte_perm(sw.z, sw.w, pick)};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int j = jp * P + i + k;
+              const uint32_t u = w0[i + k], v = w1[i + k], us = u >> 8, vs = v >> 8;
+              float d[4];
+              mma16_zero(d, u & 0x000f000fu, v & 0x000f000fu, us & 0x000f000fu, vs & 0x000f000fu, qb[j][0], qb[j][1]);
+              mma16(d, u & 0x00f000f0u, v & 0x00f000f0u, us & 0x00f000f0u, vs & 0x00f000f0u, qb[j][2], qb[j][3]);
+              const float2 sc = unpack_half2(pair[k]);
+              y[0] = fmaf(sc.x, d[0], y[0]);
+              y[1] = fmaf(sc.x, d[1], y[1]);
+              y[2] = fmaf(sc.y, d[2], y[2]);
+              y[3] = fmaf(sc.y, d[3], y[3]);
+            }
           }
         }
+        const uint32_t z0 = *reinterpret_cast<const uint32_t *>(cell + C::kKeyZero + C::key_zero_at(g, (2 * t) % NG));
+        const uint32_t z1 = *reinterpret_cast<const uint32_t *>(cell + C::kKeyZero + C::key_zero_at(g + 8, (2 * t) % NG));
+        float d[4];
+        mma16_zero(d, z0, z1, z0, z1, qz[0], qz[1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[ce][i] = fmaf(0x1p-18f, d[i], y[i]);
       }
-      {
-        float d[4] = {0.f, 0.f, 0.f, 0.f};
-        const int zg = (2 * t) % NG;
-        const uint32_t z0 = *reinterpret_cast<const uint32_t *>(cell + C::kKeyZero + C::key_zero_at(g, zg));
-        const uint32_t z1 = *reinterpret_cast<const uint32_t *>(cell + C::kKeyZero + C::key_zero_at(g + 8, zg));
-        mma16(d, z0, z1, z0, z1, qz[0], qz[1]);
-        x[0] = fmaf(c1[0], x[0], c2[0] * d[0]);
-        x[1] = fmaf(c1[1], x[1], c2[1] * d[1]);
-        x[2] = fmaf(c1[0], x[2], c2[0] * d[2]);
-        x[3] = fmaf(c1[1], x[3], c2[1] * d[3]);
-      }
-      if (valid < kCell) {
-        if (g >= valid) x[0] = x[1] = -kInf;
-        if (g + 8 >= valid) x[2] = x[3] = -kInf;
+      // masked slots
+      bool none[kStep][2];
+#pragma unroll
+      for (int ce = 0; ce < kStep; ++ce) {
+        none[ce][0] = ce * kCell + g >= valid;
+        none[ce][1] = ce * kCell + g + 8 >= valid;
       }
 
-      // ---- value scales and zeros of tokens g and g + 8
-      uint32_t vs[NG], vz[NG];
+      // ---- the reference: every scale below 2^E, every x at most M + kTop + kSlack - E
+      uint32_t top = 0;
 #pragma unroll
-      for (int j = 0; j < NG; j += 2) {
-        const uint4 sw = *reinterpret_cast<const uint4 *>(cell + C::kValScale + C::scale_at(g & 7, j) - 2 * (g & 1));
-        vs[j] = __byte_perm(sw.x, sw.y, pick);
-        vs[j + 1] = __byte_perm(sw.z, sw.w, pick);
-        const uint4 zw = *reinterpret_cast<const uint4 *>(cell + C::kValZero + C::scale_at(g & 7, j) - 2 * (g & 1));
-        vz[j] = __byte_perm(zw.x, zw.y, pick);
-        vz[j + 1] = __byte_perm(zw.z, zw.w, pick);
-      }
-      // exponent e with every scale of the two tokens below 2^e
-      uint32_t top = vs[0];
+      for (int ce = 0; ce < kStep; ++ce)
 #pragma unroll
-      for (int j = 1; j < NG; ++j) top = __vmaxu2(top, vs[j]);
+        for (int j = 0; j < NG; j += 2) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(stage + ce * C::kBytes + C::kValScale + C::scale_at(2 * t, j));
+          top = __vmaxu2(__vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w)), top);
+        }
       top = max(top & 0xffffu, top >> 16);
-      const float e = (float)((int)(top >> 10) - 14);
-      float need[2] = {fmaxf(x[0], x[2]) + e - kTop, fmaxf(x[1], x[3]) + e - kTop};
-      if (__any_sync(0xffffffffu, need[0] > M[0] + kSlack || need[1] > M[1] + kSlack)) {
+      int e = (int)(top >> 10) - 14;
+      float p[kStep][4], far = -kInf;  // x - M
+#pragma unroll
+      for (int ce = 0; ce < kStep; ++ce)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          p[ce][i] = fmaf(c1[0], x[ce][i], -M[0]);
+          p[ce][i + 1] = fmaf(c1[1], x[ce][i + 1], -M[1]);
+          if (none[ce][i / 2]) p[ce][i] = p[ce][i + 1] = -kInf;
+          far = max3f(far, p[ce][i], p[ce][i + 1]);
+        }
+      if (__any_sync(0xffffffffu, far > kTop + kSlack - (float)E || e > E)) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+        const float up = (float)(max(e, E) - E);
+        E = max(e, E);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+          float big = -kInf;
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) need[i] = fmaxf(need[i], __shfl_xor_sync(0xffffffffu, need[i], o));
-          need[i] = fmaxf(need[i], M[i]);
-          const float f = M[i] == -kInf ? 0.f : exp2f(M[i] - need[i]);
-          M[i] = need[i];
-          l[i] *= f;
+          for (int ce = 0; ce < kStep; ++ce)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) big = none[ce][o] ? big : fmaxf(big, c1[i] * x[ce][2 * o + i]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+          const float to = fmaxf(big - kTop + (float)E, M[i] + up);
+          const float f = M[i] == -kInf ? 0.f : exp2f(M[i] - to);
+          M[i] = to;
+          zs[i] *= f;
+          zs[i + 2] *= f;
 #pragma unroll
           for (int k = 0; k < 2 * NG; ++k) {
             acc[k][i] *= f;
             acc[k][i + 2] *= f;
           }
 #pragma unroll
-          for (int j = 0; j < NG; ++j) zs[j][i] *= f;
+          for (int ce = 0; ce < kStep; ++ce)
+#pragma unroll
+            for (int o = 0; o < 2; ++o) p[ce][2 * o + i] = none[ce][o] ? -kInf : fmaf(c1[i], x[ce][2 * o + i], -to);
         }
       }
-      float p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = ex2_approx(x[i] - M[i & 1]);
-      l[0] += p[0] + p[2];
-      l[1] += p[1] + p[3];
 
       // ---- values
 #pragma unroll
-      for (int jp = 0; jp < NG / P; ++jp) {
-        uint32_t w0[P], w1[P];
-        const uint8_t *v0 = cell + C::val_half(2 * t, jp * P, g), *v1 = cell + C::val_half(2 * t + 8, jp * P, g);
-        if constexpr (P == 4) {
-          const uint4 u = *reinterpret_cast<const uint4 *>(v0), v = *reinterpret_cast<const uint4 *>(v1);
-          w0[0] = u.x; w0[1] = u.y; w0[2] = u.z; w0[3] = u.w;
-          w1[0] = v.x; w1[1] = v.y; w1[2] = v.z; w1[3] = v.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2 *>(v0), v = *reinterpret_cast<const uint2 *>(v1);
-          w0[0] = u.x; w0[1] = u.y;
-          w1[0] = v.x; w1[1] = v.y;
-        }
+      for (int ce = 0; ce < kStep; ++ce) {
+        const uint8_t *const cell = stage + ce * C::kBytes;
+        // tokens 2 t, 2 t + 1 (and + 8) of head g
+        uint32_t ph[2], pl[2];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          const int j = jp * P + i;
-          const float2 sc = unpack_half2(vs[j]), ze = unpack_half2(vz[j]);
-          zs[j][0] = fmaf(p[0], ze.x, fmaf(p[2], ze.y, zs[j][0]));
-          zs[j][1] = fmaf(p[1], ze.x, fmaf(p[3], ze.y, zs[j][1]));
-          const float y[4] = {p[0] * sc.x, p[1] * sc.x, p[2] * sc.y, p[3] * sc.y};
-          const uint32_t h0 = pack_half2(y[0], y[1]), h1 = pack_half2(y[2], y[3]);
-          const uint32_t b0 = transpose8(h0), b1 = transpose8(h1);
-          const uint32_t u = w0[i], v = w1[i], us = u >> 8, vv = v >> 8;
-          mma16(acc[2 * j], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
-          mma16(acc[2 * j + 1], us & 0x000f000fu, us & 0x00f000f0u, vv & 0x000f000fu, vv & 0x00f000f0u, b0, b1);
+        for (int o = 0; o < 2; ++o) {
+          const float p0 = ex2_approx(p[ce][2 * o]), p1 = ex2_approx(p[ce][2 * o + 1]);
+          const uint32_t w = pack_half2(p0, p1);
+          ph[o] = transpose8(w);
           if constexpr (kTwoParts) {
-            const float2 r0 = unpack_half2(h0), r1 = unpack_half2(h1);
-            const uint32_t q0 = transpose8(pack_half2(y[0] - r0.x, y[1] - r0.y));
-            const uint32_t q1 = transpose8(pack_half2(y[2] - r1.x, y[3] - r1.y));
-            mma16(acc[2 * j], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, q0, q1);
-            mma16(acc[2 * j + 1], us & 0x000f000fu, us & 0x00f000f0u, vv & 0x000f000fu, vv & 0x00f000f0u, q0, q1);
+            const float2 r = unpack_half2(w);
+            pl[o] = transpose8(pack_half2(p0 - r.x, p1 - r.y));
+          }
+        }
+        uint2 z = make_uint2(0u, 0u);
+        if (g < NG) z = *reinterpret_cast<const uint2 *>(cell + C::kValZero + C::scale_at(2 * t, g % NG));
+        mma16(zs, z.x, ones, z.y, ones, ph[0], ph[1]);
+        if constexpr (kTwoParts) mma16(zs, z.x, ones, z.y, ones, pl[0], pl[1]);
+#pragma unroll
+        for (int jp = 0; jp < NG / P; ++jp) {
+          uint32_t w0[P], w1[P];
+          load_words(w0, cell + C::val_half(2 * t, jp * P, g));
+          load_words(w1, cell + C::val_half(2 * t + 8, jp * P, g));
+#pragma unroll
+          for (int i = 0; i < P; i += 2) {
+            const uint4 sw = *reinterpret_cast<const uint4 *>(cell + C::kValScale + C::scale_at(2 * t, jp * P + i));
+            const uint32_t sc[2][2] = {{sw.x, sw.y}, {sw.z, sw.w}};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int j = jp * P + i + k;
+              const uint32_t u = w0[i + k], v = w1[i + k], us = u >> 8, vs = v >> 8;
+              uint32_t b0, b1;
+              if constexpr (kTwoParts) {
+                const float2 s0 = unpack_half2(sc[k][0]), s1 = unpack_half2(sc[k][1]);
+                const float2 h0 = unpack_half2(ph[0]), h1 = unpack_half2(ph[1]), l0 = unpack_half2(pl[0]), l1 = unpack_half2(pl[1]);
+                const float y[4] = {(h0.x + l0.x) * s0.x, (h0.y + l0.y) * s0.y, (h1.x + l1.x) * s1.x, (h1.y + l1.y) * s1.y};
+                b0 = pack_half2(y[0], y[1]);
+                b1 = pack_half2(y[2], y[3]);
+                const float2 r0 = unpack_half2(b0), r1 = unpack_half2(b1);
+                const uint32_t q0 = pack_half2(y[0] - r0.x, y[1] - r0.y), q1 = pack_half2(y[2] - r1.x, y[3] - r1.y);
+                mma16(acc[2 * j], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, q0, q1);
+                mma16(acc[2 * j + 1], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, q0, q1);
+              } else {
+                b0 = mul_half2(ph[0], sc[k][0]);
+                b1 = mul_half2(ph[1], sc[k][1]);
+              }
+              mma16(acc[2 * j], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
+              mma16(acc[2 * j + 1], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, b0, b1);
+            }
           }
         }
       }
     }
 
     // ---- merge the part across the warps
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
+    if (bad && lane == 0) atomicOr(a.c.errors, TQ_ERRF_PAGE);
+    if (g == 0)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-#pragma unroll
-        for (int j = 0; j < NG; ++j) zs[j][i] += __shfl_xor_sync(0xffffffffu, zs[j][i], o);
+        state[(warp * 8 + 2 * t + i) * 2] = M[i];
+        state[(warp * 8 + 2 * t + i) * 2 + 1] = bad || dead ? __int_as_float(0x7fffffff) : zs[2 + i];
       }
-    }
-    if (bad || dead) l[0] = l[1] = __int_as_float(0x7fffffff);
-    if (bad && lane == 0) atomicOr(a.c.errors, TQ_ERRF_PAGE);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int h = 2 * t + i;
-      if (h < G) {
-        if (g == 0) {
-          state[(warp * 8 + h) * 2] = M[i];
-          state[(warp * 8 + h) * 2 + 1] = l[i];
-        }
-        float *o = merge + (size_t)(warp * G + h) * D + 4 * g;
+    for (int j = 0; j < NG; ++j) {
+      const float z[2] = {__shfl_sync(0xffffffffu, zs[0], 4 * j + t), __shfl_sync(0xffffffffu, zs[1], 4 * j + t)};
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          const float w = 16777216.f, z = zs[j][i];
-          *reinterpret_cast<float4 *>(o + 32 * j) =
-              make_float4(fmaf(acc[2 * j][i], w, z), fmaf(acc[2 * j][i + 2], w * 0.0625f, z), fmaf(acc[2 * j + 1][i], w, z),
-                          fmaf(acc[2 * j + 1][i + 2], w * 0.0625f, z));
-        }
+      for (int i = 0; i < 2; ++i) {
+        const float w = 16777216.f;
+        if (2 * t + i < G)
+          *reinterpret_cast<float4 *>(merge + (size_t)(warp * G + 2 * t + i) * D + 32 * j + 4 * g) =
+              make_float4(fmaf(acc[2 * j][i], w, z[i]), fmaf(acc[2 * j][i + 2], w * 0.0625f, z[i]),
+                          fmaf(acc[2 * j + 1][i], w, z[i]), fmaf(acc[2 * j + 1][i + 2], w * 0.0625f, z[i]));
       }
     }
     __syncthreads();
-    const bool whole = here.cell == 0 && end - at == here.cells;
+    const bool whole = here.step == 0 && end - at == here.steps;
     float *const part = a.partials + ((size_t)blockIdx.x * 2 + (at == 0 ? 0 : 1)) * G * (D + 4);
     for (int i = tid; i < G * D / 4; i += kThreads) {
       const int h = i / (D / 4), c = 4 * (i % (D / 4));
@@ -542,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       }
     }
     __syncthreads();
-    here.cell += end - at;
+    here.step += end - at;
     at = end;
     if (at < count) here.settle(a.c);
   }
@@ -560,16 +634,16 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
   const int b = blockIdx.x / a.c.h_kv, h = blockIdx.x % a.c.h_kv, tid = threadIdx.x;
   const int G = a.h_q / a.c.h_kv;
   long long before, total;
-  sum_cells(a.c, b, scan, &before, &total);
-  const int cells = cells_of(a.c, b);
+  sum_steps(a.c, b, scan, &before, &total);
+  const int steps = steps_of(a.c, b);
   T *const out = reinterpret_cast<T *>(a.out) + (size_t)b * a.out_stride + (size_t)h * G * D;
-  if (cells == 0) {
+  if (steps == 0) {
     pdl_wait();
     for (int i = tid; i < G * D / 8; i += 128) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
     return;
   }
-  const long long per = range_cells(total, blocks);
-  const long long u0 = before + (long long)h * cells, u1 = u0 + cells;
+  const long long per = range_steps(total, blocks);
+  const long long u0 = before + (long long)h * steps, u1 = u0 + steps;
   const int first = (int)(u0 / per), last = (int)((u1 - 1) / per), n = last - first + 1;
   pdl_wait();
   if (n == 1) return;
