@@ -4,17 +4,19 @@
 // copy rate an SM receives one cell (16 tokens of a KV head, 20 d bytes) every
 // ~110 cycles at d = 128, so a warp scheduler has ~440 issue slots a cell.
 //
-// Split.  All cells of the batch, in the order (sequence, KV head, position),
-// are cut into equal contiguous ranges, one per block (two blocks an SM, one
-// at d = 256), so ragged lengths leave no tail; a range's warps take its cells
-// in turn.  The part of a unit (sequence, KV head) that a range holds is
-// merged across the warps; a unit inside one range goes straight to the
-// output, the parts of the others (at most two a range: its first and its
-// last) to the workspace, where paged_combine_kernel joins them in order.
+// Split.  All steps (pairs of cells) of the batch, in the order (sequence, KV
+// head, position), are cut into equal contiguous ranges, one per block (two
+// blocks an SM, one at d = 256), and a range into equal parts for its warps,
+// so ragged lengths leave no tail.  A warp works through its part alone: units
+// (sequence, KV head) that lie inside it go straight to the output; of the
+// others it leaves at most two (its first and its last) in shared memory,
+// which the block joins once at its end.  A unit that spans blocks goes to the
+// workspace in at most two records a block, which paged_combine_kernel joins
+// in order.
 //
-// A warp is its own pipeline: one lane keeps the next cells' bulk copies in
-// flight into the warp's ring, with the page number loaded one cell earlier
-// still, so no warp waits for another inside a range.
+// A warp is its own pipeline: one lane keeps the next step's bulk copy in
+// flight into the warp's ring, with the page number loaded one step earlier
+// still, so no warp waits for another.
 //
 // Products.  The codes enter the tensor cores as they are stored: a 4-bit
 // field in the low bits of a half is the subnormal n 2^-24 (or n 2^-20 one
@@ -57,14 +59,22 @@ constexpr float kTop = 10.f, kSlack = 4.f;  // p 2^E <= 2^10 when M moves, < 2^1
 
 __host__ __device__ constexpr int blocks_per_sm(int d) { return d == 256 ? 1 : 2; }
 
+// What a warp leaves of a unit: its place, and which of the unit's ends it has.
+struct Record {
+  int b, h;
+  int ends;   // 1: the unit's first step, 2: its last
+  int place;  // -1: none; else the first step, counted from the block's range
+};
+
 template <int D>
 struct Smem {
   static constexpr int kStage = kStep * Cell<D>::kBytes;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kBars = kRing;                            // [kWarps][kStages] u64
   static constexpr int kScan = kBars + kWarps * kStages * 8;     // 16 long long
-  static constexpr int kState = kScan + 128;                     // [kWarps][8][2] floats: M, l
-  static constexpr int kMerge = kState + kWarps * 8 * 2 * 4;     // [kWarps][G][D] floats
+  static constexpr int kInfo = kScan + 128;                      // [kWarps][2] Record
+  static constexpr int kState = kInfo + kWarps * 2 * 16;         // [kWarps][8][2] floats: M, l of the first records
+  static constexpr int kMerge = kState + kWarps * 8 * 2 * 4;     // [kWarps][G][D] floats: their sums
   static constexpr size_t bytes(int G) { return kMerge + (size_t)kWarps * G * D * 4; }
 };
 
@@ -184,7 +194,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
   constexpr int NG = C::kGroups, P = C::kP;
   constexpr bool kTwoParts = __is_same(T, __half);
   extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int g = lane >> 2, t = lane & 3;
   const int G = a.h_q / a.c.h_kv;
   uint8_t *const ring = smem + warp * kStages * S::kStage;
@@ -199,18 +209,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     fence_mbar_init();
   }
   // ---- this block's range, and the sequence it starts in
-  long long total, unused;
-  sum_steps(a.c, 0, scan, &unused, &total);
-  pdl_trigger();
-  const long long per = range_steps(total, gridDim.x);
-  const long long c0 = per * blockIdx.x;
-  if (c0 >= total) return;
-  const int count = (int)(min(c0 + per, total) - c0);
+  long long total, c0, per;
   {
-    long long base = 0;
-    for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
-      const int b = b0 + tid;
-      const long long n = b < a.c.batch ? (long long)steps_of(a.c, b) * a.c.h_kv : 0;
+    // inclusive sum over the block's threads: sequences base + tid
+    auto prefix = [&](int base, long long n, long long *all) {
       long long inc = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -219,34 +221,58 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       }
       if (lane == 31) scan[warp] = inc;
       __syncthreads();
-      long long ahead = base, all = base;
+      long long sum = 0;
+#pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) ahead += scan[w];
-        all += scan[w];
+        if (w < warp) inc += scan[w];
+        sum += scan[w];
       }
+      *all = sum;
+      return inc;
+    };
+    long long n = tid < a.c.batch ? (long long)steps_of(a.c, tid) * a.c.h_kv : 0, all;
+    long long inc = prefix(0, n, &all);
+    total = all;
+    if (a.c.batch > kThreads) {
+      long long unused;
       __syncthreads();
-      if (ahead + inc > c0 && ahead + inc - n <= c0) {
-        scan[8] = b;
-        scan[9] = ahead + inc - n;
+      sum_steps(a.c, 0, scan, &unused, &total);
+    }
+    pdl_trigger();
+    per = range_steps(total, gridDim.x);
+    c0 = per * blockIdx.x;
+    if (c0 >= total) return;
+    long long before = 0;
+    for (int b0 = 0;;) {
+      if (before + inc > c0 && before + inc - n <= c0) {
+        scan[8] = b0 + tid;
+        scan[9] = before + inc - n;
       }
-      base = all;
-      if (base > c0) break;
+      before += all;
+      b0 += kThreads;
+      if (before > c0 || b0 >= a.c.batch) break;
+      __syncthreads();
+      n = b0 + tid < a.c.batch ? (long long)steps_of(a.c, b0 + tid) * a.c.h_kv : 0;
+      inc = prefix(b0, n, &all);
     }
     __syncthreads();
   }
-  Cursor here;  // the range's first step
-  here.b = (int)scan[8];
-  here.steps = steps_of(a.c, here.b);
-  here.h = (int)((c0 - scan[9]) / here.steps);
-  here.step = (int)((c0 - scan[9]) % here.steps);
+  const int count = (int)(min(c0 + per, total) - c0);
+  // the warp's part: steps [at, stop) of the range
+  int at = (int)((long long)count * warp / kWarps);
+  const int stop = (int)((long long)count * (warp + 1) / kWarps), mine = stop - at;
+  Cursor here;  // step `at`
+  // (broadcast from one lane: what the whole warp shares can stay in uniform registers)
+  here.b = __shfl_sync(0xffffffffu, (int)scan[8], 0);
+  here.steps = __shfl_sync(0xffffffffu, steps_of(a.c, here.b), 0);
+  const int into = __shfl_sync(0xffffffffu, (int)(c0 - scan[9]), 0);
+  here.h = into / here.steps;
+  here.step = into % here.steps + at;
+  if (mine > 0) here.settle(a.c);
 
-  // ---- the warp's copies: steps warp, warp + kWarps, .. of the range.  The
-  // page of a step's cells (one page where pages hold two cells or more) is
-  // looked up a step before their copy.
+  // ---- the warp's copies.  The page of a step's cells (one page where pages
+  // hold two cells or more) is looked up a step before their copy.
   Cursor next = here;
-  next.step += warp;
-  next.settle(a.c);
-  const int mine = count > warp ? (count - warp + kWarps - 1) / kWarps : 0;
   const int per_page = a.c.page_shift - 4;  // log2 of the cells of a page
   const uint32_t head_bytes = (uint32_t)C::kBytes << per_page;
   const size_t page_bytes = (size_t)head_bytes * a.c.h_kv;
@@ -288,8 +314,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       }
     }
     if (++asked < mine) {
-      next.step += kWarps;
-      if (next.step >= next.steps) {
+      if (++next.step >= next.steps) {
         const int was = next.b;
         next.settle(a.c);
         if (next.b != was) enter();
@@ -301,13 +326,15 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
   issue();
 
   int used = 0;       // steps taken
-  int at = 0;         // first step of the current part, counted from the range's start
+  Record *const info = reinterpret_cast<Record *>(smem + S::kInfo);
+  if (lane < 2) info[2 * warp + lane].place = -1;
+  const int begin = at;
   bool dead = false;  // a wait ran out
   const float kInf = INFINITY;
 
-  while (at < count) {
-    // ---- one part: steps [at, end) of the range, all of unit (here.b, here.h)
-    const int end = min(count, at + here.steps - here.step);
+  while (at < stop) {
+    // ---- steps [at, end) of the range, all of unit (here.b, here.h)
+    const int end = min(stop, at + here.steps - here.step);
     const int len = a.c.len[here.b];
     bool bad = len > (a.c.max_pages << a.c.page_shift);
 
@@ -380,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
 
-    for (int idx = used * kWarps + warp; idx < end && !dead; idx += kWarps, ++used) {
+    for (int idx = at; idx < end && !dead; ++idx, ++used) {
       __syncwarp();
       issue();
       const int s = used % kStages;
@@ -565,48 +592,93 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       }
     }
 
-    // ---- merge the part across the warps
+    // ---- a unit that is all here goes to the output, the rest to a record
     if (bad && lane == 0) atomicOr(a.c.errors, TQ_ERRF_PAGE);
-    if (g == 0)
+    if (bad || dead) zs[2] = zs[3] = __int_as_float(0x7fffffff);
+    const int ends = (here.step == 0 ? 1 : 0) | (here.step + end - at == here.steps ? 2 : 0);
+    const int slot = 2 * warp + (at == begin ? 0 : 1);
+    // the last record lies in the warp's own ring, whose copies have all been used
+    float *const rec = at == begin ? merge + (size_t)warp * G * D : reinterpret_cast<float *>(ring);
+    float *const rec_state = at == begin ? state + warp * 16 : rec + G * D;
+    if (ends != 3) {
+      __syncwarp();
+      if (g == 0)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        state[(warp * 8 + 2 * t + i) * 2] = M[i];
-        state[(warp * 8 + 2 * t + i) * 2 + 1] = bad || dead ? __int_as_float(0x7fffffff) : zs[2 + i];
-      }
+        for (int i = 0; i < 2; ++i)
+          if (2 * t + i < G) {
+            rec_state[2 * (2 * t + i)] = M[i];
+            rec_state[2 * (2 * t + i) + 1] = zs[2 + i];
+          }
+      if (lane == 0) info[slot] = Record{here.b, here.h, ends, at};
+    }
+    const float sum[2] = {__shfl_sync(0xffffffffu, zs[2], t), __shfl_sync(0xffffffffu, zs[3], t)};
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
       const float z[2] = {__shfl_sync(0xffffffffu, zs[0], 4 * j + t), __shfl_sync(0xffffffffu, zs[1], 4 * j + t)};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float w = 16777216.f;
-        if (2 * t + i < G)
-          *reinterpret_cast<float4 *>(merge + (size_t)(warp * G + 2 * t + i) * D + 32 * j + 4 * g) =
-              make_float4(fmaf(acc[2 * j][i], w, z[i]), fmaf(acc[2 * j][i + 2], w * 0.0625f, z[i]),
-                          fmaf(acc[2 * j + 1][i], w, z[i]), fmaf(acc[2 * j + 1][i + 2], w * 0.0625f, z[i]));
+        if (2 * t + i < G) {
+          const float4 o = make_float4(fmaf(acc[2 * j][i], w, z[i]), fmaf(acc[2 * j][i + 2], w * 0.0625f, z[i]),
+                                       fmaf(acc[2 * j + 1][i], w, z[i]), fmaf(acc[2 * j + 1][i + 2], w * 0.0625f, z[i]));
+          if (ends != 3) {
+            *reinterpret_cast<float4 *>(rec + (2 * t + i) * D + 32 * j + 4 * g) = o;
+          } else {
+            const float r = 1.f / sum[i];
+            T *out = reinterpret_cast<T *>(a.out) + (size_t)here.b * a.out_stride + (size_t)(here.h * G + 2 * t + i) * D;
+            *reinterpret_cast<uint2 *>(out + 32 * j + 4 * g) = make_uint2(pack2<T>(o.x * r, o.y * r), pack2<T>(o.z * r, o.w * r));
+          }
+        }
       }
     }
-    __syncthreads();
-    const bool whole = here.step == 0 && end - at == here.steps;
-    float *const part = a.partials + ((size_t)blockIdx.x * 2 + (at == 0 ? 0 : 1)) * G * (D + 4);
+    here.step += end - at;
+    at = end;
+    if (at < stop) here.settle(a.c);
+  }
+  // a warp that gave up still waits for its own copies
+  if (dead)
+    for (int i = used; i < asked; ++i) mbar_wait(&bars[i % kStages], (i / kStages) & 1);
+
+  // ---- the block joins its warps' records: runs of one unit, in order
+  __syncthreads();
+  for (int r = 0; r < 2 * kWarps;) {
+    const Record first = info[r];
+    if (first.place < 0) {
+      ++r;
+      continue;
+    }
+    int last = r, ends = first.ends;
+    for (int k = r + 1; k < 2 * kWarps; ++k) {
+      const Record next = info[k];
+      if (next.place < 0) continue;
+      if (next.b != first.b || next.h != first.h) break;
+      last = k;
+      ends |= next.ends;
+    }
+    float *const part = a.partials + ((size_t)blockIdx.x * 2 + (first.place == 0 ? 0 : 1)) * G * (D + 4);
     for (int i = tid; i < G * D / 4; i += kThreads) {
       const int h = i / (D / 4), c = 4 * (i % (D / 4));
-      float top = -kInf;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, state[(w * 8 + h) * 2]);
-      float sum = 0.f;
+      float top = -kInf, sum = 0.f;
+      auto sums = [&](int k) {
+        return k & 1 ? reinterpret_cast<const float *>(smem + (k / 2) * kStages * S::kStage) : merge + (size_t)(k / 2) * G * D;
+      };
+      auto states = [&](int k) { return (k & 1 ? sums(k) + G * D : state + (k / 2) * 16) + 2 * h; };
+      for (int k = r; k <= last; ++k)
+        if (info[k].place >= 0) top = fmaxf(top, states(k)[0]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(state[(w * 8 + h) * 2] - top);
-        const float4 v = *reinterpret_cast<const float4 *>(merge + (size_t)(w * G + h) * D + c);
-        sum = fmaf(f, state[(w * 8 + h) * 2 + 1], sum);
+#pragma unroll 4
+      for (int k = r; k <= last; ++k) {
+        if (info[k].place < 0) continue;
+        const float f = exp2f(states(k)[0] - top);
+        const float4 v = *reinterpret_cast<const float4 *>(sums(k) + h * D + c);
+        sum = fmaf(f, states(k)[1], sum);
         o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
         o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
       }
-      if (whole) {
-        const float r = 1.f / sum;
-        T *out = reinterpret_cast<T *>(a.out) + (size_t)here.b * a.out_stride + (size_t)(here.h * G + h) * D + c;
-        *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(o.x * r, o.y * r), pack2<T>(o.z * r, o.w * r));
+      if (ends == 3) {
+        const float q = 1.f / sum;
+        T *out = reinterpret_cast<T *>(a.out) + (size_t)first.b * a.out_stride + (size_t)(first.h * G + h) * D + c;
+        *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<T>(o.x * q, o.y * q), pack2<T>(o.z * q, o.w * q));
       } else {
         *reinterpret_cast<float4 *>(part + h * D + c) = o;
         if (c == 0) {
@@ -615,31 +687,27 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
         }
       }
     }
-    __syncthreads();
-    here.step += end - at;
-    at = end;
-    if (at < count) here.settle(a.c);
+    r = last + 1;
   }
-  // a warp that gave up still waits for its own copies
-  if (dead)
-    for (int i = used; i < asked; ++i) mbar_wait(&bars[i % kStages], (i / kStages) & 1);
 }
 
-// Joins the parts of each unit that more than one range holds; zeros for
-// empty sequences.  One block a unit.
+// Joins the records of each unit that more than one range holds; zeros for
+// empty sequences.  One block a query head: four warps share the records, a
+// lane holds D / 32 channels.
 template <int D, class T>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constant__ PagedDecodeArgs a, int blocks) {
+  constexpr int E = D / 32;
   __shared__ long long scan[16];
-  __shared__ float wt[8][512];
-  const int b = blockIdx.x / a.c.h_kv, h = blockIdx.x % a.c.h_kv, tid = threadIdx.x;
-  const int G = a.h_q / a.c.h_kv;
+  __shared__ float parts[4][D];
+  const int hq = blockIdx.x % a.h_q, b = blockIdx.x / a.h_q, G = a.h_q / a.c.h_kv, h = hq / G;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   long long before, total;
   sum_steps(a.c, b, scan, &before, &total);
   const int steps = steps_of(a.c, b);
-  T *const out = reinterpret_cast<T *>(a.out) + (size_t)b * a.out_stride + (size_t)h * G * D;
+  T *const out = reinterpret_cast<T *>(a.out) + (size_t)b * a.out_stride + (size_t)hq * D;
   if (steps == 0) {
     pdl_wait();
-    for (int i = tid; i < G * D / 8; i += 128) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tid; i < D / 8; i += 128) reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
     return;
   }
   const long long per = range_steps(total, blocks);
@@ -647,42 +715,40 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const __grid_constan
   const int first = (int)(u0 / per), last = (int)((u1 - 1) / per), n = last - first + 1;
   pdl_wait();
   if (n == 1) return;
-  // the unit is the last part of its first range unless that range starts with it
-  auto part = [&](int i) {
-    const int slot = i == 0 && u0 % per != 0 ? 1 : 0;
-    return a.partials + ((size_t)(first + i) * 2 + slot) * G * (D + 4);
-  };
-  __shared__ float tops[8], sums[8];
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int hq = warp; hq < G; hq += 4) {
-    float top = -INFINITY, sum = 0.f;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, part(i)[G * D + 2 * hq]);
-    top = warp_max(top);
-    for (int i = lane; i < n; i += 32) {
-      const float f = exp2f(part(i)[G * D + 2 * hq] - top);
-      if (i < 512) wt[hq][i] = f;
-      sum = fmaf(f, part(i)[G * D + 2 * hq + 1], sum);
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) {
-      tops[hq] = top;
-      sums[hq] = sum;
+  // the unit is the second record of its first range unless that range starts with it
+  const size_t size = (size_t)G * (D + 4);
+  const float *const base = a.partials + (size_t)first * 2 * size;
+  const int from0 = u0 % per != 0 ? 1 : 0, head = hq % G;
+  auto record = [&](int i) { return base + (size_t)(2 * i + (i == 0 ? from0 : 0)) * size; };
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, record(i)[G * D + 2 * head]);
+  top = warp_max(top);
+  float o[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += 4) {
+    const float *p = record(i);
+    const float f = exp2f(p[G * D + 2 * head] - top);
+    sum = fmaf(f, p[G * D + 2 * head + 1], sum);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2 *>(p + head * D + 32 * e + 2 * lane);
+      o[e] = fmaf(f, v.x, o[e]);
+      o[e + 1] = fmaf(f, v.y, o[e + 1]);
     }
   }
+#pragma unroll
+  for (int e = 0; e < E; e += 2) *reinterpret_cast<float2 *>(&parts[warp][32 * e + 2 * lane]) = make_float2(o[e], o[e + 1]);
+  __shared__ float sums[4];
+  if (lane == 0) sums[warp] = sum;
   __syncthreads();
-  for (int i = tid; i < G * D / 4; i += 128) {
-    const int hq = i / (D / 4), c = 4 * (i % (D / 4));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float *p = part(k);
-      const float f = k < 512 ? wt[hq][k] : exp2f(p[G * D + 2 * hq] - tops[hq]);
-      const float4 v = *reinterpret_cast<const float4 *>(p + hq * D + c);
-      o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
-    }
-    const float r = 1.f / sums[hq];
-    *reinterpret_cast<uint2 *>(out + hq * D + c) = make_uint2(pack2<T>(o.x * r, o.y * r), pack2<T>(o.z * r, o.w * r));
+  const float r = 1.f / (sums[0] + sums[1] + sums[2] + sums[3]);
+  for (int c = 2 * tid; c < D; c += 256) {
+    float y[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y[i] = (parts[0][c + i] + parts[1][c + i] + parts[2][c + i] + parts[3][c + i]) * r;
+    *reinterpret_cast<uint32_t *>(out + c) = pack2<T>(y[0], y[1]);
   }
 }
 
@@ -698,7 +764,7 @@ cudaError_t launch(const PagedDecodeArgs &a, cudaStream_t stream) {
   kernel<<<blocks, kThreads, smem, stream>>>(a, wait_limit_ns());
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_combine_kernel<D, T>, dim3(a.c.batch * a.c.h_kv), dim3(128), 0, stream, a, blocks);
+  return launch_pdl(paged_combine_kernel<D, T>, dim3(a.c.batch * a.h_q), dim3(128), 0, stream, a, blocks);
 }
 
 }  // namespace
