@@ -66,23 +66,28 @@ __device__ __forceinline__ uint8_t *cell_ptr(const PagedView &c, int p, int pos,
   return c.data + at * Cell<D>::kBytes;
 }
 
-// Packed rows grouped by cell: sequence b, whose rows are cu[b] .. cu[b + 1]
-// - 1 at positions first .. , owns the units [(cu[b] >> 4) + 2 b, (cu[b + 1]
-// >> 4) + 2 (b + 1)), one per cell that its rows touch; n rows touch at most
-// (n + 14) / 16 + 1 <= n / 16 + 2 cells, and the range has at least n / 16 + 2
-// units, so no prefix sum is needed.  cu is clamped to [0, rows].
+// Packed rows grouped by spans of 2^S positions: sequence b, whose rows are
+// cu[b] .. cu[b + 1] - 1 at positions first .. , owns the units [(cu[b] >> S) +
+// 2 b, (cu[b + 1] >> S) + 2 (b + 1)), one per span that its rows touch; n rows
+// touch at most (n + 2^S - 2) / 2^S + 1 <= n / 2^S + 2 spans, and the range has
+// at least n / 2^S + 2 units, so no prefix sum is needed.  cu is clamped to
+// [0, rows].
 __device__ __forceinline__ int clamp_cu(const int32_t *cu, int b, int rows) { return min(max(cu[b], 0), rows); }
-__host__ __device__ __forceinline__ long long cell_units(int rows, int batch) { return (rows >> 4) + 2ll * batch; }
+template <int S>
+__host__ __device__ __forceinline__ long long span_units(int rows, int batch) {
+  return (rows >> S) + 2ll * batch;
+}
 
 // Sequence that owns unit u.  Warp-cooperative 32-way search: every lane
 // probes one of 32 equal steps (one round per factor of 32 in the batch).
+template <int S>
 __device__ __forceinline__ int unit_sequence(const int32_t *cu, int batch, int rows, int u) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = batch;
   while (n > 1) {
     const int step = (n + 31) >> 5;
     const int at = lane * step;
-    const bool below = at < n && (clamp_cu(cu, lo + at, rows) >> 4) + 2 * (lo + at) <= u;
+    const bool below = at < n && (clamp_cu(cu, lo + at, rows) >> S) + 2 * (lo + at) <= u;
     const int k = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0);
     lo += k * step;
     n = min(step, n - k * step);

@@ -4,19 +4,25 @@
 // Mathematics.  A pair (a, b) of a head row turns by its position's angle; the
 // products of two values of at most 24 bits are exact in float64, so each
 // output is one float64 rounding and one to float32, whatever the order.  A
-// group's codes follow include/tq.h; the quotient is taken in float32 by the
-// scale's reciprocal (relative error below 2^-22, so at most 4e-6 at the
-// largest code) and again in float64 where it lies within 1e-5 of a rounding
-// boundary, so every code is the exact one.
+// group's codes follow include/tq.h: scale and codes are taken in float32 (the
+// quotients' relative errors stay below 2^-21, at most 7e-6 of a code) and
+// again in float64 where they lie that near a rounding boundary, so every
+// stored bit is the exact one.
 //
 // A block takes one cell (16 positions of a sequence) and one KV head, with
 // the query heads that read it: their rows share the positions, so cosines
-// and sines are loaded and widened once per thread.  A cell that the call
+// and sines are loaded and widened once per thread.  A warp takes 256 channels
+// of rows (two rows at d = 128): it has each row's piece (the group's query
+// heads, the key, the value) copied into shared memory by one bulk copy, so
+// that what is in flight does not depend on registers, and turns and encodes
+// them without waiting for the block's other warps.  A cell that the call
 // fills is put together in shared memory and stored in 16-byte pieces; one
-// that it fills in part (a decode step's single token) is stored in place,
-// as words and half words that no other token shares.
+// that it fills in part (a decode step's single token) is stored in place, as
+// words and half words that no other token shares.
 #include "paged.cuh"
+#include "sm100.cuh"
 #include "tq_common.cuh"
+#include "tq_kernels.h"
 
 namespace tq {
 namespace {
@@ -30,6 +36,19 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
+}
+
+// fp16 of (hi - lo) / 15, rounded once.  The float32 quotient decides unless
+// it lies next to a rounding boundary or below fp16's normal range.
+__device__ __forceinline__ __half group_scale(float lo, float hi) {
+  const float q = (hi - lo) * (1.f / 15.f);
+  const int low = __float_as_int(q) & 0x1fff;
+  if (abs(low - 0x1000) <= 16 || q < 0x1p-13f) {
+    // the float64 quotient, by its reciprocal and one correction
+    const double d = (double)hi - (double)lo, e = d * (1.0 / 15.0);
+    return __double2half(fma(fma(-15.0, e, d), 1.0 / 15.0, e));
+  }
+  return __float2half_rn(q);
 }
 
 // Codes of eight channels, a quarter of a group; the group's other quarters
@@ -48,165 +67,245 @@ __device__ __forceinline__ uint32_t encode8(const float (&x)[8], __half *scale, 
     hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
   }
   const __half z = __float2half_rn(lo);
-  const __half s = __double2half(((double)hi - (double)lo) / 15.0);
+  const __half s = group_scale(lo, hi);
   const float zf = __half2float(z), sf = __half2float(s);
-  const float inv = sf > 0.f ? 1.f / sf : 0.f;
+  const float inv = sf > 0.f ? __fdividef(1.f, sf) : 0.f;
+  constexpr float kInt = 8388608.f;  // 2^23: the sum's low bits are the rounded code
   uint32_t w = 0;
+  bool near = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float t = (x[i] - zf) * inv;
-    float r = rintf(t);
-    if (fabsf(t - r) > 0.5f - 1e-5f && sf > 0.f) r = (float)rint(((double)x[i] - (double)zf) / (double)sf);
-    w |= (uint32_t)fminf(fmaxf(r, 0.f), 15.f) << (4 * i);  // NaN: fmaxf gives 0
+  for (int i = 7; i >= 0; --i) {
+    const float t = fminf(fmaxf((x[i] - zf) * inv, 0.f), 15.f);  // NaN: fmaxf gives 0
+    const float m = t + kInt;
+    near |= fabsf(t - (m - kInt)) > 0.5f - 1e-5f;
+    w = (w << 4) + __float_as_uint(m);
+  }
+  w -= 0x4b000000u + 0xb0000000u;  // 2^23's bits, which the shifts have moved out but for channels 0 and 1
+  if (near) {
+    w = 0;
+#pragma unroll 1
+    for (int i = 7; i >= 0; --i) {
+      const double t = ((double)x[i] - (double)zf) / (double)sf;
+      w = w << 4 | (uint32_t)fmin(fmax(rint(t), 0.0), 15.0);
+    }
   }
   *scale = s;
   *zero = z;
   return w;
 }
 
-// D threads: thread (n, p) of row n = tid / (D / 16) rotates two chunks of
-// eight channels, a and b, which hold whole pairs.
+// Four elements as they lie in memory.
+template <class T>
+struct Raw {
+  uint32_t w[sizeof(T)];
+};
+template <class T>
+__device__ __forceinline__ void fetch(Raw<T> &r, const T *p) {
+  if constexpr (sizeof(T) == 4) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    r.w[0] = u.x; r.w[1] = u.y; r.w[2] = u.z; r.w[3] = u.w;
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    r.w[0] = u.x; r.w[1] = u.y;
+  }
+}
+template <class T>
+__device__ __forceinline__ void widen(const Raw<T> &r, float (&x)[4]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(r.w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if constexpr (__is_same(T, __half)) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&r.w[i]));
+        x[2 * i] = f.x; x[2 * i + 1] = f.y;
+      } else {
+        x[2 * i] = __uint_as_float(r.w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+      }
+    }
+  }
+}
+template <class T>
+__device__ __forceinline__ void store4(T *p, const float (&x)[4]) {
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+  else
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+}
+// Shared memory of a block: the warps' barriers, the assembled cell, the turned
+// keys in float32 (rows padded by 16 bytes) and the rows as they came.
 template <int D, class T>
-__global__ void __launch_bounds__(D) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+struct AppendSmem {
+  static constexpr int kImage = 128, kPad = D + 4;
+  static constexpr int kKeys = kImage + Cell<D>::kBytes;
+  static constexpr int kRows = kKeys + kCell * kPad * 4;
+  static constexpr size_t bytes(int G) { return kRows + (size_t)kCell * (G + 2) * D * sizeof(T); }
+};
+
+// 2 D threads: thread (n, p) of row n = tid / (D / 8) turns two chunks of four
+// channels, a and b, which hold whole pairs, and encodes eight channels.
+template <int D, class T>
+__global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
   using C = Cell<D>;
-  constexpr int kChunks = D / 8, kRowThreads = D / 16, kPad = D + 4;
-  __shared__ __align__(16) float keys[kCell * kPad];
-  __shared__ __align__(16) uint8_t image[C::kBytes];
-  const int tid = threadIdx.x;
-  const int h = blockIdx.x % a.c.h_kv;
-  const int u = blockIdx.x / a.c.h_kv;
-  const int b = unit_sequence(a.cu, a.c.batch, a.T, u);
+  using S = AppendSmem<D, T>;
+  constexpr int kChunks = D / 8, kOwn = 32 / kChunks;  // rows of a warp
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint64_t *const bar = reinterpret_cast<uint64_t *>(smem) + warp;
+  uint8_t *const image = smem + S::kImage;
+  float *const keys = reinterpret_cast<float *>(smem + S::kKeys);
+  T *const rows = reinterpret_cast<T *>(smem + S::kRows);
+  if (lane == 0) {
+    sm100::mbar_init(bar, 1);
+    sm100::fence_mbar_init();
+  }
+  const int h = blockIdx.x % a.c.h_kv, u = blockIdx.x / a.c.h_kv;
+  const int b = unit_sequence<4>(a.cu, a.c.batch, a.T, u);
   const int r0 = clamp_cu(a.cu, b, a.T), r1 = max(clamp_cu(a.cu, b + 1, a.T), r0);
   const int first = a.c.len[b] - (r1 - r0);  // position of row r0
   const int cell = (first >> 4) + u - ((r0 >> 4) + 2 * b);
   // rows of this cell: positions 16 cell .. 16 cell + 15
   const int lo = max(16 * cell, first), hi = min(16 * cell + 16, first + (r1 - r0));
   if (lo >= hi) return;
-  const int page = page_of(a.c, b, lo);
-  // tokens outside the rotation's table are not stored
-  const int last = a.rope ? min(hi, a.max_positions) : hi;
-  const bool whole = last - lo == kCell;
-  if (page < 0 && tid == 0) atomicOr(a.c.errors, TQ_ERRF_PAGE);
-  uint8_t *const cellp = page < 0 ? image : cell_ptr<D>(a.c, page, lo, h);
-  uint8_t *const to = whole ? image : cellp;
 
-  // ---- rotation
-  const int n = tid / kRowThreads, p = tid % kRowThreads;
-  const int pos = 16 * cell + n;
-  const bool live = pos >= lo && pos < hi;
-  const bool rotates = a.rope != nullptr;
-  const bool in_table = !rotates || (pos >= 0 && pos < a.max_positions);
-  if (live && !in_table && p == 0 && h == 0) atomicOr(a.c.errors, TQ_ERRF_POSITION);
-  const int half = a.rotary_dim / 2;
-  const bool turn = rotates && live && in_table && 16 * p < a.rotary_dim;
-  const bool split = turn && !a.interleaved;  // pairs (i, i + half): chunk a and chunk b
-  const int ca = split ? 8 * p : 16 * p, cb = split ? half + 8 * p : 16 * p + 8;
-  double cs[8], sn[8];
-  if (turn) {
-    float f[8];
-    const float *row = a.rope + (size_t)pos * a.rotary_dim + 8 * p;
-    load8(row, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = f[i];
-    load8(row + half, f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sn[i] = f[i];
-  }
-  auto rotate = [&](float (&x)[8], float (&y)[8]) {
-    if (!turn) {
-      if (live && !in_table)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = y[i] = __int_as_float(0x7fffffff);
-      return;
-    }
-    auto one = [](float &s, float &t, double c, double w) {
-      const double ds = s, dt = t;
-      s = (float)fma(ds, c, -(dt * w));
-      t = (float)fma(dt, c, ds * w);
-    };
-    if (split) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) one(x[i], y[i], cs[i], sn[i]);
+  // ---- the warp's rows: [row][query heads of the group, key, value][D]
+  const int G = a.q ? a.h_q / a.c.h_kv : 0, row_elems = (G + 2) * D;
+  const int own = 16 * cell + warp * kOwn;  // the warp's first position
+  const int from = max(own, lo), count = max(min(own + kOwn, hi) - from, 0);
+  __syncwarp();
+  if (lane == 0 && count > 0) sm100::mbar_arrive_expect_tx(bar, (uint32_t)(count * row_elems * sizeof(T)));
+  if (lane < 3 * count) {
+    const int pos = from + lane / 3, kind = lane % 3;
+    T *const to = rows + (pos - 16 * cell) * row_elems;
+    const size_t row = (size_t)(r0 + (pos - first));
+    if (kind == 0) {
+      if (G) sm100::bulk_g2s(to, reinterpret_cast<const T *>(a.q) + row * a.q_stride + (size_t)h * G * D, G * D * sizeof(T), bar);
+    } else if (kind == 1) {
+      sm100::bulk_g2s(to + G * D, reinterpret_cast<const T *>(a.k) + row * a.k_stride + (size_t)h * D, D * sizeof(T), bar);
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        one(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
-        one(y[2 * i], y[2 * i + 1], cs[4 + i], sn[4 + i]);
-      }
-    }
-  };
-  const size_t row = (size_t)(r0 + (pos - first));
-  float x[8], y[8];
-  if (live) {
-    const T *k = reinterpret_cast<const T *>(a.k) + row * a.k_stride + (size_t)h * D;
-    load8(k + ca, x);
-    load8(k + cb, y);
-    rotate(x, y);
-    if (a.k_out) {
-      T *o = reinterpret_cast<T *>(a.k_out) + row * a.k_out_stride + (size_t)h * D;
-      store8(o + ca, x);
-      store8(o + cb, y);
-    }
-    *reinterpret_cast<float4 *>(&keys[n * kPad + ca]) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4 *>(&keys[n * kPad + ca + 4]) = make_float4(x[4], x[5], x[6], x[7]);
-    *reinterpret_cast<float4 *>(&keys[n * kPad + cb]) = make_float4(y[0], y[1], y[2], y[3]);
-    *reinterpret_cast<float4 *>(&keys[n * kPad + cb + 4]) = make_float4(y[4], y[5], y[6], y[7]);
-    if (a.q) {
-      const int G = a.h_q / a.c.h_kv;
-      const T *q = reinterpret_cast<const T *>(a.q) + row * a.q_stride + (size_t)h * G * D;
-      T *o = reinterpret_cast<T *>(a.q_out) + row * a.q_out_stride + (size_t)h * G * D;
-      for (int g = 0; g < G; ++g) {
-        load8(q + g * D + ca, x);
-        load8(q + g * D + cb, y);
-        rotate(x, y);
-        store8(o + g * D + ca, x);
-        store8(o + g * D + cb, y);
-      }
+      sm100::bulk_g2s(to + (G + 1) * D, reinterpret_cast<const T *>(a.v) + row * a.v_stride + (size_t)h * D, D * sizeof(T), bar);
     }
   }
-  __syncthreads();
-  if (page < 0) return;
 
-  // ---- codes: units of eight channels; the four lanes of a group belong to
-  // one row, every lane takes part in the shuffles and stored rows write
+  // ---- meanwhile the page and the angles
+  const int n = tid / kChunks, p = tid % kChunks, pos = 16 * cell + n;
+  const bool live = pos >= lo && pos < hi, rotates = a.rope != nullptr;
+  const bool in_table = !rotates || (pos >= 0 && pos < a.max_positions);
+  // tokens outside the rotation's table are not stored
+  const int last = rotates ? min(hi, a.max_positions) : hi;
+  const bool stored = live && pos < last, whole = last - lo == kCell;
+  const int half = a.rotary_dim / 2;
+  const bool turn = rotates && live && in_table && 8 * p < a.rotary_dim;
+  const bool split = turn && !a.interleaved;  // pairs (i, i + half): chunk a and chunk b
+  const int ca = split ? 4 * p : 8 * p, cb = split ? half + 4 * p : 8 * p + 4;
+  double cs[4], sn[4];
+  if (turn) {
+    const float *table = a.rope + (size_t)pos * a.rotary_dim + 4 * p;
+    const float4 c = *reinterpret_cast<const float4 *>(table), s = *reinterpret_cast<const float4 *>(table + half);
+    cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
+    sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
+  }
+  const int page = page_of(a.c, b, lo);
+  if (page < 0 && tid == 0) atomicOr(a.c.errors, TQ_ERRF_PAGE);
+  if (live && !in_table && p == 0 && h == 0) atomicOr(a.c.errors, TQ_ERRF_POSITION);
+  // (a copy always lands; should a wait run out, the warp's rows stay unwritten)
+  const bool ok = count > 0 && __all_sync(0xffffffffu, sm100::mbar_wait(bar, 0));
+  if (count > 0 && !ok && lane == 0) atomicOr(a.c.errors, TQ_ERRF_QUANTIZE_WAIT);
+
+  if (ok) {
+    // ---- rotation: turns the chunks a and b of a head row
+    const T *const mine = rows + n * row_elems;
+    auto rotate = [&](const T *from, float (&x)[4], float (&y)[4]) {
+      Raw<T> ra, rb;
+      fetch(ra, from + ca);
+      fetch(rb, from + cb);
+      widen(ra, x);
+      widen(rb, y);
+      auto pair = [](float &u, float &v, double c, double w) {
+        const double s = u, t = v;
+        u = (float)fma(s, c, -(t * w));
+        v = (float)fma(t, c, s * w);
+      };
+      if (split) {
 #pragma unroll
-  for (int it = 0; it < 2; ++it) {
-    const int i = it * D + tid, m = i / kChunks, chunk = i % kChunks;
-    const int at = 16 * cell + m, j = chunk >> 2, w4 = chunk & 3;
-    const bool stored = at >= lo && at < last;
-    float kx[8], vx[8];
+        for (int i = 0; i < 4; ++i) pair(x[i], y[i], cs[i], sn[i]);
+      } else if (turn) {
+        pair(x[0], x[1], cs[0], sn[0]);
+        pair(x[2], x[3], cs[1], sn[1]);
+        pair(y[0], y[1], cs[2], sn[2]);
+        pair(y[2], y[3], cs[3], sn[3]);
+      } else if (!in_table) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) kx[e] = vx[e] = 0.f;
-    if (stored) {
-      load8(&keys[m * kPad + 8 * chunk], kx);
-      load8(reinterpret_cast<const T *>(a.v) + (size_t)(r0 + (at - first)) * a.v_stride + (size_t)h * D + 8 * chunk, vx);
+        for (int i = 0; i < 4; ++i) x[i] = y[i] = __int_as_float(0x7fffffff);
+      }
+    };
+    if (live) {
+      const size_t row = (size_t)(r0 + (pos - first));
+      float x[4], y[4];
+      rotate(mine + G * D, x, y);
+      *reinterpret_cast<float4 *>(&keys[n * S::kPad + ca]) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<float4 *>(&keys[n * S::kPad + cb]) = make_float4(y[0], y[1], y[2], y[3]);
+      if (a.k_out) {
+        T *o = reinterpret_cast<T *>(a.k_out) + row * a.k_out_stride + (size_t)h * D;
+        store4(o + ca, x);
+        store4(o + cb, y);
+      }
+      T *o = reinterpret_cast<T *>(a.q_out) + row * a.q_out_stride + (size_t)h * G * D;
+      const T *from = mine;
+#pragma unroll 2
+      for (int g = 0; g < G; ++g, o += D, from += D) {
+        rotate(from, x, y);
+        store4(o + ca, x);
+        store4(o + cb, y);
+      }
     }
-    __half ks, kz, vs, vz;
-    const uint32_t kw = encode8(kx, &ks, &kz), vw = encode8(vx, &vs, &vz);
-    if (stored) {
-      *reinterpret_cast<uint32_t *>(to + C::key_word(m, j, w4)) = kw;
-      *reinterpret_cast<uint16_t *>(to + C::val_half(m, j, 2 * w4)) = (uint16_t)vw;
-      *reinterpret_cast<uint16_t *>(to + C::val_half(m, j, 2 * w4 + 1)) = (uint16_t)(vw >> 16);
-      const int section[4] = {C::kKeyScale + C::scale_at(m, j), C::kKeyZero + C::key_zero_at(m, j),
-                              C::kValScale + C::scale_at(m, j), C::kValZero + C::scale_at(m, j)};
-      const __half number[4] = {ks, kz, vs, vz};
+    __syncwarp();
+
+    // ---- codes of channels 8 p .. + 7 of row n, keys and then values; the four
+    // lanes of a group belong to one row, every lane takes part in the shuffles
+    // and stored rows write
+    if (page >= 0) {
+      uint8_t *const to = whole ? image : cell_ptr<D>(a.c, page, lo, h);
+      const int j = p >> 2, w4 = p & 3;
+      float z[8];
+      __half scale, zero;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (w4 == e) *reinterpret_cast<__half *>(to + section[e]) = number[e];
+      for (int e = 0; e < 8; ++e) z[e] = 0.f;
+      if (stored) load8(&keys[n * S::kPad + 8 * p], z);
+      uint32_t w = encode8(z, &scale, &zero);
+      if (stored) {
+        *reinterpret_cast<uint32_t *>(to + C::key_word(n, j, w4)) = w;
+        if (w4 == 0) *reinterpret_cast<__half *>(to + C::kKeyScale + C::scale_at(n, j)) = scale;
+        if (w4 == 1) *reinterpret_cast<__half *>(to + C::kKeyZero + C::key_zero_at(n, j)) = zero;
+        load8(mine + (G + 1) * D + 8 * p, z);
+      }
+      w = encode8(z, &scale, &zero);
+      if (stored) {
+        *reinterpret_cast<uint16_t *>(to + C::val_half(n, j, 2 * w4)) = (uint16_t)w;
+        *reinterpret_cast<uint16_t *>(to + C::val_half(n, j, 2 * w4 + 1)) = (uint16_t)(w >> 16);
+        if (w4 == 2) *reinterpret_cast<__half *>(to + C::kValScale + C::scale_at(n, j)) = scale;
+        if (w4 == 3) *reinterpret_cast<__half *>(to + C::kValZero + C::scale_at(n, j)) = zero;
+      }
     }
   }
-  if (whole) {
-    __syncthreads();
-    for (int i = tid; i < C::kBytes / 16; i += D)
-      reinterpret_cast<uint4 *>(cellp)[i] = reinterpret_cast<const uint4 *>(image)[i];
+  if (whole && page >= 0) {
+    if (!__syncthreads_and(ok)) return;
+    uint4 *const to = reinterpret_cast<uint4 *>(cell_ptr<D>(a.c, page, lo, h));
+    for (int i = tid; i < C::kBytes / 16; i += 2 * D) to[i] = reinterpret_cast<const uint4 *>(image)[i];
   }
 }
 
 template <int D, class T>
 cudaError_t launch(const PagedAppendArgs &a, cudaStream_t stream) {
-  const long long blocks = cell_units(a.T, a.c.batch) * a.c.h_kv;
+  using S = AppendSmem<D, T>;
+  const long long blocks = span_units<4>(a.T, a.c.batch) * a.c.h_kv;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
-  paged_append_kernel<D, T><<<(unsigned)blocks, D, 0, stream>>>(a);
+  static std::atomic<int> allowed[kAttributeDevices];
+  const cudaError_t e = allow_smem(paged_append_kernel<D, T>, S::bytes(TQ_PAGED_MAX_GQA), allowed);
+  if (e != cudaSuccess) return e;
+  paged_append_kernel<D, T><<<(unsigned)blocks, 2 * D, S::bytes(a.q ? a.h_q / a.c.h_kv : 0), stream>>>(a);
   return cudaGetLastError();
 }
 

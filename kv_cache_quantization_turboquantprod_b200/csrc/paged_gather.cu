@@ -25,8 +25,8 @@ __global__ void __launch_bounds__(32 * kWarps) paged_gather_kernel(const __grid_
   const long long id = (long long)blockIdx.x * kWarps + warp;
   const int h = (int)(id % a.c.h_kv);
   const long long u = id / a.c.h_kv;
-  if (u >= cell_units(a.rows, a.c.batch)) return;
-  const int b = unit_sequence(a.cu, a.c.batch, a.rows, (int)u);
+  if (u >= span_units<4>(a.rows, a.c.batch)) return;
+  const int b = unit_sequence<4>(a.cu, a.c.batch, a.rows, (int)u);
   const int r0 = clamp_cu(a.cu, b, a.rows), r1 = max(clamp_cu(a.cu, b + 1, a.rows), r0);
   const int first = a.first ? a.first[b] : 0;
   const int cell = (first >> 4) + (int)u - ((r0 >> 4) + 2 * b);
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_gather_kernel(const __grid_
 
 template <int D, class T>
 cudaError_t launch(const PagedGatherArgs &a, cudaStream_t stream) {
-  const long long warps = cell_units(a.rows, a.c.batch) * a.c.h_kv;
+  const long long warps = span_units<4>(a.rows, a.c.batch) * a.c.h_kv;
   const long long blocks = (warps + kWarps - 1) / kWarps;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   paged_gather_kernel<D, T><<<(unsigned)blocks, 32 * kWarps, 0, stream>>>(a);

@@ -109,7 +109,7 @@ tq_status tq_paged_append(const tq_paged_cache *c, const tq_paged_batch *s, cons
     if (!rows_ok(q, q_stride, qrow, dtype) || !rows_ok(q_out, q_out_stride, qrow, dtype)) return TQ_ERR_INVALID_ARGUMENT;
     if (q_out == q && q_out_stride != q_stride) return TQ_ERR_INVALID_ARGUMENT;
   }
-  if (T > (1 << 30) || tq::cell_units(T, s->batch) * c->h_kv > 0x7fffffffll) return TQ_ERR_CAPACITY;
+  if (T > (1 << 30) || tq::span_units<4>(T, s->batch) * c->h_kv > 0x7fffffffll) return TQ_ERR_CAPACITY;
   tq::PagedAppendArgs a;
   if ((st = view(c, s, &a.c)) != TQ_OK) return st;
   a.rope = rope ? rope->table : nullptr;
@@ -135,7 +135,7 @@ tq_status tq_paged_gather(const tq_paged_cache *c, const tq_paged_batch *s, cons
   if (rows == 0) return TQ_OK;
   const long long row = (long long)c->h_kv * c->d;
   if (!rows_ok(k_out, k_stride, row, dtype) || !rows_ok(v_out, v_stride, row, dtype)) return TQ_ERR_INVALID_ARGUMENT;
-  if (rows > (1 << 30) || tq::cell_units(rows, s->batch) * c->h_kv > 0x7fffffffll) return TQ_ERR_CAPACITY;
+  if (rows > (1 << 30) || tq::span_units<4>(rows, s->batch) * c->h_kv > 0x7fffffffll) return TQ_ERR_CAPACITY;
   tq::PagedGatherArgs a;
   if ((st = view(c, s, &a.c)) != TQ_OK) return st;
   a.cu = cu_rows; a.first = first;
