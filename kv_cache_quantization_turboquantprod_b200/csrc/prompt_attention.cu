@@ -7,22 +7,25 @@
 //
 // Rows.  A tile's 128 rows are (token, query head of the group) pairs of one
 // KV head: 128 / G tokens with their G heads, so K and V are read once for
-// the group and short prompts fill the tile.  A block takes two such tiles
-// (one at d = 256) of one sequence and KV head and walks the keys that they
-// see, 128 at a time (64 at d = 256).
+// the group and short prompts fill the tile.  A block takes one tile and walks
+// the keys that it sees, 128 at a time (64 at d = 256).  Two blocks share an SM
+// (at d = 256 one, whose tile alternates between two S buffers): one's softmax
+// runs under the other's products, and its start and end under the other's
+// work.
 //
 // Roles.  Warp 0 has the TMA engine copy Q once and the K and V tiles through
 // a ring (128-byte swizzle, one box per 64 channels); warp 1 issues the
 // products: S = Q K^T into tensor memory, and O += P V with P read from
-// tensor memory and V as it lies (MN-major).  Each tile's four softmax warps,
-// a thread a row, read S, keep the running maximum and sum in float32, write
-// P over S in the operand type and divide at the end.  The two tiles alternate:
-// one's softmax runs under the other's products.  At d = 256 one tile
-// alternates between two S buffers instead (two tiles' O do not fit).
+// tensor memory and V as it lies (MN-major).  Eight softmax warps, two threads
+// a row (one per half of the step's keys), read S, keep the running maximum
+// and sum in float32, write P over S in the operand type and divide at the
+// end.  Two warps a scheduler: one's maxima and conversions run under the
+// other's exponentials.
 //
 // The running maximum only moves when a row's grows by more than 2^8 (P stays
-// in range of both types, and the sum in float32), so O is seldom rescaled;
-// the row's own thread does it, between the products that write and read it.
+// in range of both types, and the sum in float32), so a row's two threads
+// mostly need one barrier with a vote to agree, and O is seldom rescaled; the
+// threads do it themselves, between the products that write and read it.
 // A scale of either sign: a negative one negates Q in the product's
 // descriptor.
 //
@@ -47,18 +50,27 @@ using namespace sm100;
 
 template <int D>
 struct Prompt {
-  static constexpr int kTiles = D == 256 ? 1 : 2;   // query tiles of a block
+  static constexpr bool kTwoBufs = D == 256;        // S buffers
+  static constexpr int kBlocks = D == 256 ? 1 : 2;  // blocks of an SM
   static constexpr int kKeys = D == 256 ? 64 : 128; // keys of a step
   static constexpr int kSlabs = D / 64;             // 64-channel boxes
   static constexpr int kQSlab = 128 * 128, kSlab = kKeys * 128;
   static constexpr int kQTile = kQSlab * kSlabs, kStage = kSlab * kSlabs;
-  static constexpr int kStages = D == 64 ? 8 : 5;
-  static constexpr int kThreads = 128 + 128 * kTiles;
-  static constexpr int kBars = kTiles * kQTile + kStages * kStage;
-  static constexpr size_t kSmem = kBars + 512 + 1024;  // 1024: alignment of the base
-  // tensor memory columns: S (and P over it) of buffer x, O of tile x
+  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 2 : 5;
+  static constexpr int kThreads = 384;
+  static constexpr int kExchange = kQTile + kStages * kStage;  // [2][128] floats, [2][4] ints
+  static constexpr int kBars = kExchange + 1024 + 32;
+  static constexpr size_t kSmem = kBars + 256 + 1024;  // 1024: alignment of the base
+  // tensor memory columns: S (and P over it) of buffer x, O
+  static constexpr uint32_t kColumns = D == 256 ? 512 : 256, kO = D == 256 ? 256 : 128;
   __host__ __device__ static constexpr uint32_t s_col(int x) { return 128u * x; }
-  __host__ __device__ static constexpr uint32_t o_col(int x) { return 256u + (uint32_t)D * x; }
+  // P of keys 16 k .. + 15, from the S buffer's first column: each half over the first half of its own S
+  __host__ __device__ static constexpr uint32_t p_col(int k) {
+    return k < kKeys / 32 ? 8u * k : (uint32_t)kKeys / 2 + 8u * (k - kKeys / 32);
+  }
+  // registers of a thread: copies and products, softmax; together at most what
+  // the launch has (80 or 168 a thread)
+  static constexpr int kFew = D == 256 ? 64 : 48, kMany = D == 256 ? 216 : 96;
 };
 
 // Sequence of block u: sequence b owns blocks [cu[b] / tb + b, cu[b + 1] / tb
@@ -77,44 +89,41 @@ __device__ __forceinline__ int block_sequence(const int32_t *cu, int batch, int 
 }
 
 template <int D, class T>
-__global__ void __launch_bounds__(Prompt<D>::kThreads, 1)
+__global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
     prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int units) {
   using C = Prompt<D>;
-  constexpr int KT = C::kKeys, NQ = C::kTiles, ST = C::kStages;
-  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
+  constexpr int KT = C::kKeys, ST = C::kStages;
+  constexpr bool kBf16 = __is_same(T, __nv_bfloat16), kTwoBufs = C::kTwoBufs;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *const stages = smem + NQ * C::kQTile;
+  uint8_t *const stages = smem + C::kQTile;
+  float *const exchange = reinterpret_cast<float *>(smem + C::kExchange);
+  int *const exchange_ok = reinterpret_cast<int *>(exchange + 256);
   uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + C::kBars);
   uint64_t *const q_full = bars, *const kv_full = bars + 1, *const kv_empty = kv_full + ST, *const s_full = kv_empty + ST,
-                  *const p_ready = s_full + 2, *const o_done = p_ready + 2, *const v_last = o_done + 2,
+                  *const p_ready = s_full + 2, *const o_done = p_ready + 2, *const v_last = o_done + 1,
                   *const v_clear = v_last + 1, *const drained = v_clear + 1;
   uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  // the tile's first row and its tokens, for the end (out of the registers until then)
+  volatile int *const place = abort_flag + 1;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.h_q / a.h_kv, tpt = 128 / G, tb = tpt * NQ;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int G = a.h_q / a.h_kv, tpt = 128 / G;
 
   // ---- the block's rows and keys; later blocks of a sequence see more keys
   // and start first
   const int h = blockIdx.x % a.h_kv, u = units - 1 - (int)(blockIdx.x / a.h_kv);
-  const int b = block_sequence(a.cu_q, a.batch, a.T_q, tb, u);
+  const int b = block_sequence(a.cu_q, a.batch, a.T_q, tpt, u);
   const int q0 = clamp_cu(a.cu_q, b, a.T_q), nq = max(clamp_cu(a.cu_q, b + 1, a.T_q) - q0, 0);
-  const int i0 = (u - (q0 / tb + b)) * tb;
+  const int i0 = (u - (q0 / tpt + b)) * tpt;
   if (i0 < 0 || i0 >= nq) return;
   const int k0 = clamp_cu(a.cu_k, b, a.T_k), nk = max(clamp_cu(a.cu_k, b + 1, a.T_k) - k0, 0);
   const int shift = nk - nq;  // query i sees keys j <= i + shift
-  int steps[2], seen = 0, most = 0;  // key steps of each tile; keys and steps of the block
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int last = min(nq, i0 + (x + 1) * tpt) - 1;
-    const int keys = x < NQ && i0 + x * tpt < nq ? max(min(nk, last + 1 + shift), 0) : 0;
-    steps[x] = (keys + KT - 1) / KT;
-    seen = max(seen, keys);
-    most = max(most, steps[x]);
-  }
-  const bool clears = seen < most * KT;  // the last V tile has rows that nothing sees
+  const int seen = max(min(nk, min(nq, i0 + tpt) + shift), 0);  // keys that the tile sees
+  const int steps = (seen + KT - 1) / KT;
+  const bool clears = seen < steps * KT;  // the last V tile has rows that nothing sees
 
   if (warp == 0 && lane == 0) {
     mbar_init(q_full, 1);
@@ -124,17 +133,20 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
-      mbar_init(&p_ready[x], 4);
-      mbar_init(&o_done[x], 1);
+      mbar_init(&p_ready[x], 8);
     }
+    mbar_init(o_done, 1);
     mbar_init(v_last, 1);
     mbar_init(v_clear, 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
+    place[0] = q0 + i0;
+    place[1] = min(nq - i0, tpt);
+    place[2] = h * G;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
+    tmem_alloc(tmem_slot, C::kColumns);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -149,16 +161,14 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1)
   };
 
   if (warp < 4) {
-    if constexpr (NQ == 2) reg_dealloc<64>();
+    reg_dealloc<C::kFew>();
     if (warp == 0) {
       // ---- copies
-      if (lane == 0 && most > 0) {
-        mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * C::kSlabs * tpt * G * 128));
-        for (int x = 0; x < NQ; ++x)
-          for (int s = 0; s < C::kSlabs; ++s)
-            tma_load_4d(smem + x * C::kQTile + s * C::kQSlab, &qmap, 64 * s, 0, h, q0 + i0 + x * tpt, q_full);
-        int item = 0;
-        for (; item < 2 * most; ++item) {
+      if (lane == 0 && steps > 0) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(C::kSlabs * tpt * G * 128));
+        for (int s = 0; s < C::kSlabs; ++s) tma_load_4d(smem + s * C::kQSlab, &qmap, 64 * s, 0, h, q0 + i0, q_full);
+        int item = 0;  // K and V tiles in turn
+        for (; item < 2 * steps; ++item) {
           const int st = item % ST;
           if (item >= ST && !pipe_wait(&kv_empty[st], (item / ST - 1) & 1, abort_flag, a.wait_ns, hint, &timed_out)) break;
           mbar_arrive_expect_tx(&kv_full[st], C::kStage);
@@ -174,30 +184,31 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1)
       // ---- products
       const uint32_t is = idesc_16bit(128, KT, kBf16, false, a.negate), io = idesc_16bit(128, D, kBf16, true, false);
       const uint32_t qa = smem_u32(smem), sa = smem_u32(stages);
-      auto scores = [&](int x, int buf, int j) {  // S[buf] = Q[x] K(j)^T
+      auto release = [&](int item) { mma_commit(&kv_empty[item % ST]); };
+      auto scores = [&](int j) {  // S = Q K(j)^T
+        const int buf = kTwoBufs ? j & 1 : 0;
         const uint32_t ka = sa + ((2 * j) % ST) * C::kStage;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_f16_ss(tmem + C::s_col(buf), smem_desc_sw128(qa + x * C::kQTile + (k / 4) * C::kQSlab + (k % 4) * 32, 16, 1024),
+            mma_f16_ss(tmem + C::s_col(buf), smem_desc_sw128(qa + (k / 4) * C::kQSlab + (k % 4) * 32, 16, 1024),
                        smem_desc_sw128(ka + (k / 4) * C::kSlab + (k % 4) * 32, 16, 1024), is, k > 0);
           mma_commit(&s_full[buf]);
+          release(2 * j);
         }
         __syncwarp();
       };
-      auto values = [&](int x, int buf, int j) {  // O[x] += P[buf] V(j)
+      auto values = [&](int j) {  // O += P V(j)
+        const int buf = kTwoBufs ? j & 1 : 0;
         const uint32_t va = sa + ((2 * j + 1) % ST) * C::kStage;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            mma_f16_ts(tmem + C::o_col(x), tmem + C::s_col(buf) + 8 * k, smem_desc_sw128(va + k * 2048, C::kSlab, 1024), io,
+            mma_f16_ts(tmem + C::kO, tmem + C::s_col(buf) + C::p_col(k), smem_desc_sw128(va + k * 2048, C::kSlab, 1024), io,
                        j > 0 || k > 0);
-          mma_commit(&o_done[x]);
+          mma_commit(o_done);
+          release(2 * j + 1);
         }
-        __syncwarp();
-      };
-      auto release = [&](int item) {
-        if (elect_one()) mma_commit(&kv_empty[item % ST]);
         __syncwarp();
       };
       auto landed = [&](int item) { return wait(&kv_full[item % ST], (item / ST) & 1); };
@@ -206,61 +217,34 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1)
         if (lane == 0) mbar_arrive(v_last);
         return wait(v_clear, 0);
       };
-      bool ok = most == 0 || (wait(q_full, 0) && landed(0));
+      bool ok = steps == 0 || (wait(q_full, 0) && landed(0));
       tc_fence_after();
-      if constexpr (NQ == 2) {
-        if (ok && most > 0) {
-          if (steps[0] > 0) scores(0, 0, 0);
-          if (steps[1] > 0) scores(1, 1, 0);
-          release(0);
-        }
-        for (int j = 0; ok && j < most; ++j) {
-          ok = landed(2 * j + 1) && (j + 1 == most || landed(2 * j + 2));
-          if (ok && clears && j + 1 == most) ok = cleared();
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (ok && j < steps[x]) {
-              ok = wait(&p_ready[x], j & 1);
-              tc_fence_after();
-              if (ok) {
-                values(x, x, j);
-                if (j + 1 < steps[x]) scores(x, x, j + 1);
-              }
-            }
-          }
-          if (ok) {
-            release(2 * j + 1);
-            if (j + 1 < most) release(2 * j + 2);
-          }
-        }
-      } else {
-        if (ok && most > 0) {
-          scores(0, 0, 0);
-          release(0);
-        }
-        for (int j = 0; ok && j < most; ++j) {
-          if (j + 1 < most) {
-            ok = landed(2 * j + 2);
-            tc_fence_after();
-            if (!ok) break;
-            scores(0, (j + 1) & 1, j + 1);
-            release(2 * j + 2);
-          }
-          ok = landed(2 * j + 1) && (!clears || j + 1 < most || cleared()) && wait(&p_ready[j & 1], (j >> 1) & 1);
+      if (ok && steps > 0) scores(0);
+      for (int j = 0; ok && j < steps; ++j) {
+        if (kTwoBufs && j + 1 < steps) {
+          ok = landed(2 * j + 2);
           tc_fence_after();
-          if (ok) {
-            values(0, j & 1, j);
-            release(2 * j + 1);
-          }
+          if (!ok) break;
+          scores(j + 1);
+        }
+        ok = landed(2 * j + 1) && (!clears || j + 1 < steps || cleared()) &&
+             wait(&p_ready[kTwoBufs ? j & 1 : 0], kTwoBufs ? (j >> 1) & 1 : j & 1);
+        tc_fence_after();
+        if (!ok) break;
+        values(j);
+        if (!kTwoBufs && j + 1 < steps) {
+          ok = landed(2 * j + 2);
+          tc_fence_after();
+          if (ok) scores(j + 1);
         }
       }
       // tensor and shared memory stay until every product has finished
       if (elect_one()) mma_commit(drained);
       __syncwarp();
       mbar_wait(drained, 0);
-    } else if (warp == 2 && clears && most > 0) {
+    } else if (warp == 2 && clears && steps > 0) {
       // ---- V rows that nothing sees
-      const int item = 2 * most - 1, rows = most * KT - seen;
+      const int item = 2 * steps - 1, rows = steps * KT - seen;
       if (wait(v_last, 0)) {
         uint8_t *v = stages + (item % ST) * C::kStage + (KT - rows) * 128;
         for (int i = lane; i < rows * 8; i += 32)
@@ -272,54 +256,71 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1)
       }
     }
   } else {
-    // ---- softmax: tile x, row r
-    if constexpr (NQ == 2) reg_alloc<216>();
-    const int x = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)(warp & 3) * 32u << 16;
-    const int tok = i0 + x * tpt + r / G;
-    const bool live = r < tpt * G && tok < nq;
-    const int lim = live ? min(nk, tok + 1 + shift) : 0;      // keys this row sees
-    const int easy = min(nk, i0 + x * tpt + 1 + shift);       // keys that every row of the tile sees
+    // ---- softmax: row r, half `part` of the step's keys (and of the output's channels)
+    reg_alloc<C::kMany>();
+    constexpr int KH = KT / 2, DH = D / 2;
+    const int quarter = warp & 3, part = (warp - 4) >> 2, r = quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)quarter * 32u << 16;
+    // keys that this row sees, and that every row of the tile sees (none where rows belong to no token)
+    const int lim = r < tpt * G && i0 + r / G < nq ? min(nk, i0 + r / G + 1 + shift) : 0;
+    const int easy = tpt * G < 128 ? 0 : min(nk, i0 + 1 + shift);
     const float c = a.scale_log2;
     float m = -INFINITY, l = 0.f;
-    const int n = steps[x];
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int buf = NQ == 2 ? x : j & 1, phase = NQ == 2 ? j & 1 : (j >> 1) & 1;
-      ok = wait(&s_full[buf], phase);
-      if (!ok) break;
+    for (int j = 0; j < steps; ++j) {
+      const int buf = kTwoBufs ? j & 1 : 0;
+      ok = wait(&s_full[buf], kTwoBufs ? (j >> 1) & 1 : j & 1);
       tc_fence_after();
-      const uint32_t st = tmem + C::s_col(buf) + lanes;
-      uint32_t s[KT / 32][32];
+      const uint32_t st = tmem + C::s_col(buf) + lanes + part * KH;
+      const int vis = (j + 1) * KT > easy ? lim - j * KT - part * KH : KH;  // keys of the half that the row sees
+      // 32 scores, masked ones -inf.  (They are read twice, for the maximum and
+      // for the weights: tensor memory is nearer than the registers that all of
+      // them would take.)
+      auto load = [&](int i, uint32_t (&s)[32]) {
+        tmem_ld32(st + 32 * i, s);
+        tmem_wait_ld();
+        if (__any_sync(0xffffffffu, vis < 32 * (i + 1))) {
 #pragma unroll
-      for (int i = 0; i < KT / 32; ++i) tmem_ld32(st + 32 * i, s[i]);
-      tmem_wait_ld();
-      if ((j + 1) * KT > easy || r >= tpt * G) {
-        const int vis = lim - j * KT;
-#pragma unroll
-        for (int i = 0; i < KT; ++i)
-          if (i >= vis) s[i / 32][i % 32] = 0xff800000u;
-      }
+          for (int e = 0; e < 32; ++e)
+            if (32 * i + e >= vis) s[e] = 0xff800000u;
+        }
+      };
       float top = -INFINITY;
+      if (ok) {
 #pragma unroll
-      for (int i = 0; i < KT; i += 2)
-        top = max3f(top, __uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1]));
-      // move the maximum only where it grew by more than 2^8
-      const bool grow = (top - m) * c > 8.f;  // from -inf to anything; not from -inf to -inf
-      if (__any_sync(0xffffffffu, grow)) {
+        for (int i = 0; i < KH / 32; ++i) {
+          uint32_t s[32];
+          load(i, s);
+          float top2 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            top = max3f(top, __uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            top2 = max3f(top2, __uint_as_float(s[e + 2]), __uint_as_float(s[e + 3]));
+          }
+          top = fmaxf(top, top2);
+        }
+      }
+      // The maximum moves only where it grew by more than 2^8 (from -inf to
+      // anything; not from -inf to -inf).
+      if (named_bar_or(1 + quarter, 64, (top - m) * c > 8.f || !ok)) {
+        exchange[part * 128 + r] = top;
+        if (lane == 0) exchange_ok[part * 4 + quarter] = ok;
+        named_bar_sync(1 + quarter, 64);
+        top = fmaxf(top, exchange[(part ^ 1) * 128 + r]);
+        ok = ok && exchange_ok[(part ^ 1) * 4 + quarter];
+        if (!ok) break;
         const float was = m;
-        if (grow) m = fmaxf(m, top);
+        if ((top - m) * c > 8.f) m = top;
         const float f = was == m ? 1.f : ex2_approx((was - m) * c);  // was = -inf: 0
         l *= f;
         if (j > 0) {
-          if constexpr (NQ == 1) {
-            ok = wait(&o_done[x], (j - 1) & 1);  // (at NQ = 2 the scores were issued behind it)
-            if (!ok) break;
+          if constexpr (kTwoBufs) {  // (with one buffer the scores were issued behind it)
+            ok = wait(o_done, (j - 1) & 1);
             tc_fence_after();
           }
-          const uint32_t ot = tmem + C::o_col(x) + lanes;
+          const uint32_t ot = tmem + C::kO + lanes + part * DH;
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
+          for (int i = 0; i < DH; i += 32) {
             uint32_t o[32];
             tmem_ld32(ot + i, o);
             tmem_wait_ld();
@@ -330,52 +331,77 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1)
         }
       }
       const float mc = m == -INFINITY ? 0.f : m * c;
+      const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+      float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < KT / 32; ++i) {
-        uint32_t p[16];
-        float sum = 0.f;
+      for (int i = 0; i < KH / 32; ++i) {
+        uint32_t s[32], p[16];
+        load(i, s);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float p0 = ex2_approx(fmaf(__uint_as_float(s[i][2 * e]), c, -mc));
-          const float p1 = ex2_approx(fmaf(__uint_as_float(s[i][2 * e + 1]), c, -mc));
-          sum += p0 + p1;
-          p[e] = pack2<T>(p0, p1);
+          float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, mc2);
+          y.x = ex2_approx(y.x);
+          y.y = ex2_approx(y.y);
+          sum = add2(sum, y);
+          p[e] = pack2<T>(y.x, y.y);
         }
-        l += sum;
         tmem_st16(st + 16 * i, p);
       }
+      l += sum.x + sum.y;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_ready[buf]);
     }
-    // (at NQ = 1 the last scores do not stand behind the last product but one)
-    if (NQ == 1 && n > 1 && ok) ok = wait(&o_done[x], n & 1);
-    if (n > 0 && ok) ok = wait(&o_done[x], (n - 1) & 1);
+    // ---- the output: the halves' sums, then rows through shared memory (Q's
+    // place; no product reads it any more), 16 bytes a lane
+    if (ok) {
+      named_bar_sync(1 + quarter, 64);  // (the last exchange has been read)
+      exchange[part * 128 + r] = l;
+      named_bar_sync(1 + quarter, 64);
+      l = exchange[r] + exchange[128 + r];
+      // (with two buffers the last scores do not stand behind the last product but one)
+      if (kTwoBufs && steps > 1) ok = wait(o_done, steps & 1);
+      if (steps > 0 && ok) ok = wait(o_done, (steps - 1) & 1);
+    }
     tc_fence_after();
-    const float w = !ok ? __int_as_float(0x7fffffff) : l == 0.f ? 0.f : 1.f / l;
-    T *out = reinterpret_cast<T *>(a.out) + (size_t)(q0 + tok) * a.out_stride + (size_t)(h * G + r % G) * D;
-#pragma unroll 1
-    for (int i = 0; i < D; i += 32) {
+    // a row that sees nothing is zero whatever its product holds
+    const bool none = ok && lim <= 0;
+    const float w = !ok ? __int_as_float(0x7fffffff) : 1.f / l;
+    constexpr int NC = DH / 8;  // 16-byte pieces of a row's half
+    uint8_t *const rows = smem + (warp - 4) * 32 * NC * 16;
+#pragma unroll
+    for (int i = 0; i < DH; i += 32) {
       uint32_t o[32];
-      if (n > 0 && ok) {
-        tmem_ld32(tmem + C::o_col(x) + lanes + i, o);
+      if (steps > 0 && ok) {
+        tmem_ld32(tmem + C::kO + lanes + part * DH + i, o);
         tmem_wait_ld();
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0;
       }
-      if (live) {
-        // a row that sees nothing is zero whatever its product holds
-        const bool none = lim <= 0 && ok;
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          float y[8];
+      for (int e = 0; e < 32; e += 8) {
+        uint32_t y[4];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) y[k] = none ? 0.f : __uint_as_float(o[e + k]) * w;
-          store8(out + i + e, y);
-        }
+        for (int k = 0; k < 4; ++k)
+          y[k] = none ? 0u : pack2<T>(__uint_as_float(o[e + 2 * k]) * w, __uint_as_float(o[e + 2 * k + 1]) * w);
+        const int piece = (i + e) / 8;
+        *reinterpret_cast<uint4 *>(rows + (lane * NC + (piece ^ (lane & (NC < 8 ? NC - 1 : 7)))) * 16) =
+            make_uint4(y[0], y[1], y[2], y[3]);
       }
+    }
+    __syncwarp();
+    const int group = a.h_q / a.h_kv, tok = r / group;
+    const long long mine =
+        tok < place[1] ? (long long)(place[0] + tok) * a.out_stride + (long long)(place[2] + r - tok * group) * D + part * DH : -1;
+#pragma unroll 4
+    for (int i = lane; i < 32 * NC; i += 32) {
+      const int row = i / NC, piece = i % NC;
+      const long long at = __shfl_sync(0xffffffffu, mine, row);
+      if (at >= 0)
+        *reinterpret_cast<uint4 *>(reinterpret_cast<T *>(a.out) + at + piece * 8) =
+            *reinterpret_cast<const uint4 *>(rows + (row * NC + (piece ^ (row & (NC < 8 ? NC - 1 : 7)))) * 16);
     }
   }
   if (timed_out) atomicOr(a.errors, TQ_ERRF_PROMPT_WAIT);
@@ -383,7 +409,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::kColumns);
   }
 }
 
@@ -428,8 +454,8 @@ bool encode(CUtensorMap *map, const void *p, long long stride, int heads, int pe
 template <int D, class T>
 cudaError_t launch(const PromptArgs &a, cudaStream_t stream) {
   using C = Prompt<D>;
-  const int G = a.h_q / a.h_kv, tpt = 128 / G, tb = tpt * C::kTiles;
-  const long long units = a.T_q / tb + (long long)a.batch;
+  const int G = a.h_q / a.h_kv, tpt = 128 / G;
+  const long long units = a.T_q / tpt + (long long)a.batch;
   if (units * a.h_kv > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   CUtensorMap q, k, v;
   // with no keys at all the K and V maps are never read: any rows will do
