@@ -50,20 +50,21 @@ using namespace sm100;
 
 template <int D>
 struct Prompt {
-  static constexpr bool kTwoBufs = D == 256;        // S buffers
+  static constexpr bool kTwoBufs = true;            // S buffers
   static constexpr int kBlocks = D == 256 ? 1 : 2;  // blocks of an SM
-  static constexpr int kKeys = D == 256 ? 64 : 128; // keys of a step
+  static constexpr int kKeys = 64;                  // keys of a step
+  static constexpr bool kHalves = kKeys == 128;     // P is handed over in two halves
   static constexpr int kSlabs = D / 64;             // 64-channel boxes
   static constexpr int kQSlab = 128 * 128, kSlab = kKeys * 128;
   static constexpr int kQTile = kQSlab * kSlabs, kStage = kSlab * kSlabs;
-  static constexpr int kStages = D == 64 ? 4 : D == 128 ? 2 : 5;
+  static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 5;
   static constexpr int kThreads = 384;
   static constexpr int kExchange = kQTile + kStages * kStage;  // [2][128] floats, [2][4] ints
   static constexpr int kBars = kExchange + 1024 + 32;
   static constexpr size_t kSmem = kBars + 256 + 1024;  // 1024: alignment of the base
   // tensor memory columns: S (and P over it) of buffer x, O
-  static constexpr uint32_t kColumns = D == 256 ? 512 : 256, kO = D == 256 ? 256 : 128;
-  __host__ __device__ static constexpr uint32_t s_col(int x) { return 128u * x; }
+  static constexpr uint32_t kColumns = D == 256 ? 512 : 256, kO = 2 * kKeys;
+  __host__ __device__ static constexpr uint32_t s_col(int x) { return (uint32_t)kKeys * x; }
   // P of keys 16 k .. + 15, from the S buffer's first column: each half over the first half of its own S
   __host__ __device__ static constexpr uint32_t p_col(int k) {
     return k < kKeys / 32 ? 8u * k : (uint32_t)kKeys / 2 + 8u * (k - kKeys / 32);
@@ -72,6 +73,27 @@ struct Prompt {
   // the launch has (80 or 168 a thread)
   static constexpr int kFew = D == 256 ? 64 : 48, kMany = D == 256 ? 216 : 96;
 };
+
+// 2^y for two y in [-inf, 9] (or NaN) without the exponential unit: y is cut
+// into an integer and a rest in [-1/2, 1/2], whose power is the polynomial of
+// degree 5 with the least largest relative error there (by Remez' exchange;
+// 2^-22 in float32).  Below 2^-127 the result is 0.
+__device__ __forceinline__ float2 exp2_poly(float2 y) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y.x) : "f"(-127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y.y) : "f"(-127.f));
+  auto both = [](float v) { return make_float2(v, v); };
+  const float2 t = add2(y, both(12582912.f));  // 1.5 2^23: the integer in the low bits
+  const float2 n = add2(t, both(-12582912.f));
+  const float2 f = fma2(n, both(-1.f), y);
+  float2 p = fma2(both(0x1.5c08e4p-10f), f, both(0x1.3d0c52p-7f));
+  p = fma2(p, f, both(0x1.c6b6e4p-5f));
+  p = fma2(p, f, both(0x1.ebf918p-3f));
+  p = fma2(p, f, both(0x1.62e428p-1f));
+  p = fma2(p, f, both(0x1.000002p+0f));
+  p.x *= __int_as_float((__float_as_int(t.x) << 23) + 0x3f800000);
+  p.y *= __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000);
+  return p;
+}
 
 // Sequence of block u: sequence b owns blocks [cu[b] / tb + b, cu[b + 1] / tb
 // + b + 1), at least as many as its rows need (32-way search, warp-wide).
@@ -102,7 +124,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
   int *const exchange_ok = reinterpret_cast<int *>(exchange + 256);
   uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + C::kBars);
   uint64_t *const q_full = bars, *const kv_full = bars + 1, *const kv_empty = kv_full + ST, *const s_full = kv_empty + ST,
-                  *const p_ready = s_full + 2, *const o_done = p_ready + 2, *const v_last = o_done + 1,
+                  *const p_ready = s_full + 2, *const p_half = p_ready + 2, *const o_done = p_half + 1, *const v_last = o_done + 1,
                   *const v_clear = v_last + 1, *const drained = v_clear + 1;
   uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
@@ -135,6 +157,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
       mbar_init(&s_full[x], 1);
       mbar_init(&p_ready[x], 8);
     }
+    mbar_init(p_half, 8);
     mbar_init(o_done, 1);
     mbar_init(v_last, 1);
     mbar_init(v_clear, 1);
@@ -198,16 +221,20 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
         }
         __syncwarp();
       };
-      auto values = [&](int j) {  // O += P V(j)
+      // O += P V(j) over the first 32 keys of each half, over the others, or over all
+      auto values = [&](int j, int which) {
         const int buf = kTwoBufs ? j & 1 : 0;
         const uint32_t va = sa + ((2 * j + 1) % ST) * C::kStage;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < KT / 16; ++k)
-            mma_f16_ts(tmem + C::kO, tmem + C::s_col(buf) + C::p_col(k), smem_desc_sw128(va + k * 2048, C::kSlab, 1024), io,
-                       j > 0 || k > 0);
-          mma_commit(o_done);
-          release(2 * j + 1);
+            if (which == 2 || (k >> 1 & 1) == which)
+              mma_f16_ts(tmem + C::kO, tmem + C::s_col(buf) + C::p_col(k), smem_desc_sw128(va + k * 2048, C::kSlab, 1024), io,
+                         j > 0 || k > 0);
+          if (which) {
+            mma_commit(o_done);
+            release(2 * j + 1);
+          }
         }
         __syncwarp();
       };
@@ -227,11 +254,16 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
           if (!ok) break;
           scores(j + 1);
         }
-        ok = landed(2 * j + 1) && (!clears || j + 1 < steps || cleared()) &&
-             wait(&p_ready[kTwoBufs ? j & 1 : 0], kTwoBufs ? (j >> 1) & 1 : j & 1);
+        ok = landed(2 * j + 1) && (!clears || j + 1 < steps || cleared());
+        if (C::kHalves && ok) {
+          ok = wait(p_half, j & 1);
+          tc_fence_after();
+          if (ok) values(j, 0);
+        }
+        ok = ok && wait(&p_ready[kTwoBufs ? j & 1 : 0], kTwoBufs ? (j >> 1) & 1 : j & 1);
         tc_fence_after();
         if (!ok) break;
-        values(j);
+        values(j, C::kHalves ? 1 : 2);
         if (!kTwoBufs && j + 1 < steps) {
           ok = landed(2 * j + 2);
           tc_fence_after();
@@ -261,9 +293,9 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
     constexpr int KH = KT / 2, DH = D / 2;
     const int quarter = warp & 3, part = (warp - 4) >> 2, r = quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)quarter * 32u << 16;
-    // keys that this row sees, and that every row of the tile sees (none where rows belong to no token)
-    const int lim = r < tpt * G && i0 + r / G < nq ? min(nk, i0 + r / G + 1 + shift) : 0;
-    const int easy = tpt * G < 128 ? 0 : min(nk, i0 + 1 + shift);
+    // keys that this row sees, and that every row of the tile sees (rows that
+    // belong to no token go on as if they did; nothing reads them)
+    const int lim = min(nk, i0 + r / G + 1 + shift), easy = min(nk, i0 + 1 + shift);
     const float c = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -340,12 +372,22 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, mc2);
-          y.x = ex2_approx(y.x);
-          y.y = ex2_approx(y.y);
+          if (D < 256 && e % 4 == 3) {  // a quarter of them, so that neither unit waits for the other
+            y = exp2_poly(y);
+          } else {
+            y.x = ex2_approx(y.x);
+            y.y = ex2_approx(y.y);
+          }
           sum = add2(sum, y);
           p[e] = pack2<T>(y.x, y.y);
         }
         tmem_st16(st + 16 * i, p);
+        if (C::kHalves && i == 0) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_half);
+        }
       }
       l += sum.x + sum.y;
       tmem_wait_st();
@@ -360,9 +402,9 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
       exchange[part * 128 + r] = l;
       named_bar_sync(1 + quarter, 64);
       l = exchange[r] + exchange[128 + r];
-      // (with two buffers the last scores do not stand behind the last product but one)
-      if (kTwoBufs && steps > 1) ok = wait(o_done, steps & 1);
-      if (steps > 0 && ok) ok = wait(o_done, (steps - 1) & 1);
+      // (not o_done: by now it may stand one or two products behind the last,
+      // and a parity cannot tell the last but one from the one after the last)
+      if (steps > 0) ok = wait(drained, 0);
     }
     tc_fence_after();
     // a row that sees nothing is zero whatever its product holds
