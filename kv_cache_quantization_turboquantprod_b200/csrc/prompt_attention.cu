@@ -1,31 +1,33 @@
 // tq_prompt_attention: causal attention of packed sequences with grouped
 // heads on the fifth-generation tensor cores.
 //
-// Bound: the tensor pipe (4 d flops a visible pair and query head) and, next
-// to it, the exponentials: a 128 x 128 score tile is 1024 cycles of products
-// at d = 128 and 1024 cycles of the SM's 16 exponentials a cycle.
+// Bound: the tensor pipe (4 d flops a visible pair and query head; a 128 x 128
+// score tile is 1024 cycles of products at d = 128), beside it the SM's 16
+// exponentials a cycle (1024 cycles a tile) and shared memory's 128 bytes a
+// cycle (a product of 128 rows x 128 keys reads its operands in the 64 cycles
+// that it takes, one of 64 keys in 48 for 32).
 //
 // Rows.  A tile's 128 rows are (token, query head of the group) pairs of one
 // KV head: 128 / G tokens with their G heads, so K and V are read once for
-// the group and short prompts fill the tile.  A block takes one tile and walks
-// the keys that it sees, 128 at a time (64 at d = 256).  Two blocks share an SM
-// (at d = 256 one, whose tile alternates between two S buffers): one's softmax
-// runs under the other's products, and its start and end under the other's
-// work.
+// the group and short prompts fill the tile.  A block walks the keys that its
+// one or two tiles see (struct Prompt: two shapes).
 //
 // Roles.  Warp 0 has the TMA engine copy Q once and the K and V tiles through
 // a ring (128-byte swizzle, one box per 64 channels); warp 1 issues the
 // products: S = Q K^T into tensor memory, and O += P V with P read from
-// tensor memory and V as it lies (MN-major).  Eight softmax warps, two threads
-// a row (one per half of the step's keys), read S, keep the running maximum
-// and sum in float32, write P over S in the operand type and divide at the
-// end.  Two warps a scheduler: one's maxima and conversions run under the
-// other's exponentials.
+// tensor memory and V as it lies (MN-major).  Eight softmax warps a tile, two
+// threads a row (one per half of the step's keys), read S, keep the running
+// maximum and sum in float32, write P over S in the operand type and divide at
+// the end.  One tile's softmax runs under the other's products, or one step's
+// under the next one's (two S buffers); P is handed over in halves where a
+// step has 128 keys, so that products start under the second half's
+// exponentials; a quarter of these are polynomials.
 //
 // The running maximum only moves when a row's grows by more than 2^8 (P stays
 // in range of both types, and the sum in float32), so a row's two threads
 // mostly need one barrier with a vote to agree, and O is seldom rescaled; the
 // threads do it themselves, between the products that write and read it.
+//
 // A scale of either sign: a negative one negates Q in the product's
 // descriptor.
 //
@@ -48,30 +50,35 @@ namespace {
 
 using namespace sm100;
 
-template <int D>
+// A block's shape.  NQ = 2: two tiles share the keys, 128 a step, one S buffer
+// each, one block an SM.  NQ = 1: one tile, 64 keys a step, two S buffers, two
+// blocks an SM (one at d = 256).
+template <int D, int NQ>
 struct Prompt {
-  static constexpr bool kTwoBufs = true;            // S buffers
-  static constexpr int kBlocks = D == 256 ? 1 : 2;  // blocks of an SM
-  static constexpr int kKeys = 64;                  // keys of a step
+  static_assert(D < 256 || NQ == 1, "two tiles' O do not fit beside S");
+  static constexpr bool kTwoBufs = NQ == 1;         // S buffers of a tile
+  static constexpr int kBlocks = NQ == 2 || D == 256 ? 1 : 2;  // blocks of an SM
+  static constexpr int kKeys = NQ == 2 ? 128 : 64;  // keys of a step
   static constexpr bool kHalves = kKeys == 128;     // P is handed over in two halves
   static constexpr int kSlabs = D / 64;             // 64-channel boxes
   static constexpr int kQSlab = 128 * 128, kSlab = kKeys * 128;
   static constexpr int kQTile = kQSlab * kSlabs, kStage = kSlab * kSlabs;
-  static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 5;
-  static constexpr int kThreads = 384;
-  static constexpr int kExchange = kQTile + kStages * kStage;  // [2][128] floats, [2][4] ints
-  static constexpr int kBars = kExchange + 1024 + 32;
-  static constexpr size_t kSmem = kBars + 256 + 1024;  // 1024: alignment of the base
-  // tensor memory columns: S (and P over it) of buffer x, O
-  static constexpr uint32_t kColumns = D == 256 ? 512 : 256, kO = 2 * kKeys;
+  static constexpr int kStages = D == 64 ? 8 : D == 128 ? (NQ == 2 ? 5 : 4) : 5;
+  static constexpr int kThreads = 128 + 256 * NQ;
+  static constexpr int kExchange = NQ * kQTile + kStages * kStage;  // [NQ][2][128] floats, [NQ][2][4] ints
+  static constexpr int kBars = kExchange + NQ * (1024 + 32);
+  static constexpr size_t kSmem = kBars + 256;
+  // tensor memory columns: S (and P over it) of buffer or tile x, O of tile x
+  static constexpr uint32_t kColumns = kBlocks == 2 ? 256 : 512;
   __host__ __device__ static constexpr uint32_t s_col(int x) { return (uint32_t)kKeys * x; }
+  __host__ __device__ static constexpr uint32_t o_col(int x) { return 2u * kKeys + (uint32_t)D * x; }
   // P of keys 16 k .. + 15, from the S buffer's first column: each half over the first half of its own S
   __host__ __device__ static constexpr uint32_t p_col(int k) {
     return k < kKeys / 32 ? 8u * k : (uint32_t)kKeys / 2 + 8u * (k - kKeys / 32);
   }
   // registers of a thread: copies and products, softmax; together at most what
-  // the launch has (80 or 168 a thread)
-  static constexpr int kFew = D == 256 ? 64 : 48, kMany = D == 256 ? 216 : 96;
+  // the launch has (96, 80 or 168 a thread)
+  static constexpr int kFew = NQ == 2 || D == 256 ? 64 : 48, kMany = NQ == 2 ? 104 : D == 256 ? 216 : 96;
 };
 
 // 2^y for two y in [-inf, 9] (or NaN) without the exponential unit: y is cut
@@ -110,42 +117,44 @@ __device__ __forceinline__ int block_sequence(const int32_t *cu, int batch, int 
   return lo;
 }
 
-template <int D, class T>
-__global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
+template <int D, class T, int NQ>
+__global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlocks)
     prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int units) {
-  using C = Prompt<D>;
+  using C = Prompt<D, NQ>;
   constexpr int KT = C::kKeys, ST = C::kStages;
   constexpr bool kBf16 = __is_same(T, __nv_bfloat16), kTwoBufs = C::kTwoBufs;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint8_t *const stages = smem + C::kQTile;
+  extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms)
+  uint8_t *const stages = smem + NQ * C::kQTile;
   float *const exchange = reinterpret_cast<float *>(smem + C::kExchange);
-  int *const exchange_ok = reinterpret_cast<int *>(exchange + 256);
+  int *const exchange_ok = reinterpret_cast<int *>(exchange + NQ * 256);
   uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + C::kBars);
+  // [2]: by buffer (NQ = 1) or by tile
   uint64_t *const q_full = bars, *const kv_full = bars + 1, *const kv_empty = kv_full + ST, *const s_full = kv_empty + ST,
-                  *const p_ready = s_full + 2, *const p_half = p_ready + 2, *const o_done = p_half + 1, *const v_last = o_done + 1,
-                  *const v_clear = v_last + 1, *const drained = v_clear + 1;
+                  *const p_ready = s_full + 2, *const p_half = p_ready + 2, *const o_done = p_half + 2,
+                  *const v_last = o_done + 1, *const v_clear = v_last + 1, *const drained = v_clear + 1;
   uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  // the tile's first row and its tokens, for the end (out of the registers until then)
+  // the block's first row and its tokens, for the end (out of the registers until then)
   volatile int *const place = abort_flag + 1;
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const int G = a.h_q / a.h_kv, tpt = 128 / G;
+  const int G = a.h_q / a.h_kv, tpt = 128 / G, tb = tpt * NQ;
 
   // ---- the block's rows and keys; later blocks of a sequence see more keys
   // and start first
   const int h = blockIdx.x % a.h_kv, u = units - 1 - (int)(blockIdx.x / a.h_kv);
-  const int b = block_sequence(a.cu_q, a.batch, a.T_q, tpt, u);
+  const int b = block_sequence(a.cu_q, a.batch, a.T_q, tb, u);
   const int q0 = clamp_cu(a.cu_q, b, a.T_q), nq = max(clamp_cu(a.cu_q, b + 1, a.T_q) - q0, 0);
-  const int i0 = (u - (q0 / tpt + b)) * tpt;
+  const int i0 = (u - (q0 / tb + b)) * tb;
   if (i0 < 0 || i0 >= nq) return;
   const int k0 = clamp_cu(a.cu_k, b, a.T_k), nk = max(clamp_cu(a.cu_k, b + 1, a.T_k) - k0, 0);
   const int shift = nk - nq;  // query i sees keys j <= i + shift
-  const int seen = max(min(nk, min(nq, i0 + tpt) + shift), 0);  // keys that the tile sees
-  const int steps = (seen + KT - 1) / KT;
-  const bool clears = seen < steps * KT;  // the last V tile has rows that nothing sees
+  // steps of a tile; keys that the block sees, and its steps (the last tile with rows has most)
+  auto keys_of = [&](int x) { return i0 + x * tpt < nq ? max(min(nk, min(nq, i0 + (x + 1) * tpt) + shift), 0) : 0; };
+  auto steps_of = [&](int x) { return (keys_of(x) + KT - 1) / KT; };
+  const int seen = max(keys_of(0), NQ == 2 ? keys_of(1) : 0), most = (seen + KT - 1) / KT;
+  const bool clears = seen < most * KT;  // the last V tile has rows that nothing sees
 
   if (warp == 0 && lane == 0) {
     mbar_init(q_full, 1);
@@ -156,15 +165,15 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_ready[x], 8);
+      mbar_init(&p_half[x], 8);
     }
-    mbar_init(p_half, 8);
     mbar_init(o_done, 1);
     mbar_init(v_last, 1);
     mbar_init(v_clear, 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     place[0] = q0 + i0;
-    place[1] = min(nq - i0, tpt);
+    place[1] = min(nq - i0, tb);
     place[2] = h * G;
     fence_mbar_init();
   }
@@ -175,7 +184,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   const unsigned int hint = (unsigned int)(a.wait_ns < 1000000ull ? a.wait_ns : 1000000ull);
   bool timed_out = false;
   // for a whole warp: its lanes go on, or give up, together
@@ -187,11 +196,13 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
     reg_dealloc<C::kFew>();
     if (warp == 0) {
       // ---- copies
-      if (lane == 0 && steps > 0) {
-        mbar_arrive_expect_tx(q_full, (uint32_t)(C::kSlabs * tpt * G * 128));
-        for (int s = 0; s < C::kSlabs; ++s) tma_load_4d(smem + s * C::kQSlab, &qmap, 64 * s, 0, h, q0 + i0, q_full);
+      if (lane == 0 && most > 0) {
+        mbar_arrive_expect_tx(q_full, (uint32_t)(NQ * C::kSlabs * tpt * G * 128));
+        for (int x = 0; x < NQ; ++x)
+          for (int s = 0; s < C::kSlabs; ++s)
+            tma_load_4d(smem + x * C::kQTile + s * C::kQSlab, &qmap, 64 * s, 0, h, q0 + i0 + x * tpt, q_full);
         int item = 0;  // K and V tiles in turn
-        for (; item < 2 * steps; ++item) {
+        for (; item < 2 * most; ++item) {
           const int st = item % ST;
           if (item >= ST && !pipe_wait(&kv_empty[st], (item / ST - 1) & 1, abort_flag, a.wait_ns, hint, &timed_out)) break;
           mbar_arrive_expect_tx(&kv_full[st], C::kStage);
@@ -204,79 +215,115 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
         for (int i = max(0, item - ST); i < item; ++i) mbar_wait(&kv_full[i % ST], (i / ST) & 1);
       }
     } else if (warp == 1) {
-      // ---- products
+      // ---- products.  The whole warp runs the loop, so that descriptors stay in
+      // uniform registers; one lane issues.
+      const bool leader = elect_one();
       const uint32_t is = idesc_16bit(128, KT, kBf16, false, a.negate), io = idesc_16bit(128, D, kBf16, true, false);
-      const uint32_t qa = smem_u32(smem), sa = smem_u32(stages);
-      auto release = [&](int item) { mma_commit(&kv_empty[item % ST]); };
-      auto scores = [&](int j) {  // S = Q K(j)^T
-        const int buf = kTwoBufs ? j & 1 : 0;
-        const uint32_t ka = sa + ((2 * j) % ST) * C::kStage;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_f16_ss(tmem + C::s_col(buf), smem_desc_sw128(qa + (k / 4) * C::kQSlab + (k % 4) * 32, 16, 1024),
-                       smem_desc_sw128(ka + (k / 4) * C::kSlab + (k % 4) * 32, 16, 1024), is, k > 0);
-          mma_commit(&s_full[buf]);
-          release(2 * j);
-        }
-        __syncwarp();
-      };
-      // O += P V(j) over the first 32 keys of each half, over the others, or over all
-      auto values = [&](int j, int which) {
-        const int buf = kTwoBufs ? j & 1 : 0;
-        const uint32_t va = sa + ((2 * j + 1) % ST) * C::kStage;
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < KT / 16; ++k)
-            if (which == 2 || (k >> 1 & 1) == which)
-              mma_f16_ts(tmem + C::kO, tmem + C::s_col(buf) + C::p_col(k), smem_desc_sw128(va + k * 2048, C::kSlab, 1024), io,
-                         j > 0 || k > 0);
-          if (which) {
-            mma_commit(o_done);
-            release(2 * j + 1);
+      const uint32_t sa = smem_u32(stages);
+      const uint64_t qd = smem_desc_sw128(smem_u32(smem), 16, 1024), kd = smem_desc_sw128(sa, 16, 1024),
+                     vd = smem_desc_sw128(sa, C::kSlab, 1024);
+      // where the next K and V tile lie in the ring: items 0, 2, .. and 1, 3, ..
+      struct Place {
+        int st;
+        uint32_t phase;
+        __device__ __forceinline__ void advance() {
+          st += 2;
+          if (st >= ST) {
+            st -= ST;
+            phase ^= 1;
           }
         }
-        __syncwarp();
+      } kp{0, 0}, vp{1, 0};
+      auto scores = [&](int x, int buf) {  // S[buf] = Q[x] K^T
+        const uint64_t kt = kd + (uint32_t)(kp.st * (C::kStage >> 4));
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          if (leader)
+            mma_f16_ss(tmem + C::s_col(buf), qd + (uint32_t)((x * C::kQTile + (k / 4) * C::kQSlab + (k % 4) * 32) >> 4),
+                       kt + (uint32_t)(((k / 4) * C::kSlab + (k % 4) * 32) >> 4), is, k > 0);
+        if (leader) mma_commit(&s_full[buf]);
       };
-      auto landed = [&](int item) { return wait(&kv_full[item % ST], (item / ST) & 1); };
+      // O[x] += P V over the first 32 keys of each half, over the others, or over all
+      auto values = [&](int x, int buf, int j, int which) {
+        const uint64_t vt = vd + (uint32_t)(vp.st * (C::kStage >> 4));
+#pragma unroll
+        for (int k = 0; k < KT / 16; ++k)
+          if (which == 2 || (k >> 1 & 1) == which) {
+            if (leader)
+              mma_f16_ts(tmem + C::o_col(x), tmem + C::s_col(buf) + C::p_col(k), vt + (uint32_t)(k * 128), io, j > 0 || k > 0);
+          }
+        if (kTwoBufs && leader) mma_commit(o_done);
+      };
+      auto release = [&](Place &p) {
+        if (leader) mma_commit(&kv_empty[p.st]);
+        p.advance();
+      };
+      auto landed = [&](const Place &p) { return wait(&kv_full[p.st], p.phase); };
       // the last V tile goes to warp 2 first
       auto cleared = [&] {
         if (lane == 0) mbar_arrive(v_last);
         return wait(v_clear, 0);
       };
-      bool ok = steps == 0 || (wait(q_full, 0) && landed(0));
+      bool ok = most == 0 || (wait(q_full, 0) && landed(kp));
       tc_fence_after();
-      if (ok && steps > 0) scores(0);
-      for (int j = 0; ok && j < steps; ++j) {
-        if (kTwoBufs && j + 1 < steps) {
-          ok = landed(2 * j + 2);
+      if (ok && most > 0) {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+          if (steps_of(x) > 0) scores(x, x);
+        release(kp);
+      }
+      if constexpr (kTwoBufs) {
+        for (int j = 0; ok && j < most; ++j) {
+          if (j + 1 < most) {
+            ok = landed(kp);
+            tc_fence_after();
+            if (!ok) break;
+            scores(0, (j + 1) & 1);
+            release(kp);
+          }
+          ok = landed(vp) && (!clears || j + 1 < most || cleared()) && wait(&p_ready[j & 1], (j >> 1) & 1);
           tc_fence_after();
           if (!ok) break;
-          scores(j + 1);
+          values(0, j & 1, j, 2);
+          release(vp);
         }
-        ok = landed(2 * j + 1) && (!clears || j + 1 < steps || cleared());
-        if (C::kHalves && ok) {
-          ok = wait(p_half, j & 1);
-          tc_fence_after();
-          if (ok) values(j, 0);
-        }
-        ok = ok && wait(&p_ready[kTwoBufs ? j & 1 : 0], kTwoBufs ? (j >> 1) & 1 : j & 1);
-        tc_fence_after();
-        if (!ok) break;
-        values(j, C::kHalves ? 1 : 2);
-        if (!kTwoBufs && j + 1 < steps) {
-          ok = landed(2 * j + 2);
-          tc_fence_after();
-          if (ok) scores(j + 1);
+      } else {
+        const int steps[2] = {steps_of(0), steps_of(1)};
+        for (int j = 0; ok && j < most; ++j) {
+          // (each tile is asked for just before its first use and given back just
+          // after its last, or the copies do not come in time)
+          ok = landed(vp) && (!clears || j + 1 < most || cleared());
+          bool next = false;  // K(j + 1) is here
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (ok && j < steps[x]) {
+              ok = wait(&p_half[x], j & 1);
+              tc_fence_after();
+              if (ok) {
+                values(x, x, j, 0);
+                ok = wait(&p_ready[x], j & 1);
+                tc_fence_after();
+              }
+              if (ok) values(x, x, j, 1);
+            }
+            if (ok && x == 1) release(vp);
+            if (ok && j + 1 < steps[x]) {
+              if (!next) ok = landed(kp);
+              next = true;
+              tc_fence_after();
+              if (ok) scores(x, x);
+            }
+          }
+          if (ok && j + 1 < most) release(kp);
         }
       }
       // tensor and shared memory stay until every product has finished
-      if (elect_one()) mma_commit(drained);
+      if (leader) mma_commit(drained);
       __syncwarp();
       mbar_wait(drained, 0);
-    } else if (warp == 2 && clears && steps > 0) {
+    } else if (warp == 2 && clears && most > 0) {
       // ---- V rows that nothing sees
-      const int item = 2 * steps - 1, rows = steps * KT - seen;
+      const int item = 2 * most - 1, rows = most * KT - seen;
       if (wait(v_last, 0)) {
         uint8_t *v = stages + (item % ST) * C::kStage + (KT - rows) * 128;
         for (int i = lane; i < rows * 8; i += 32)
@@ -288,19 +335,20 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
       }
     }
   } else {
-    // ---- softmax: row r, half `part` of the step's keys (and of the output's channels)
+    // ---- softmax: tile x, row r, half `part` of the step's keys (and of the output's channels)
     reg_alloc<C::kMany>();
     constexpr int KH = KT / 2, DH = D / 2;
-    const int quarter = warp & 3, part = (warp - 4) >> 2, r = quarter * 32 + lane;
+    const int x = (warp - 4) >> 3, quarter = warp & 3, part = ((warp - 4) >> 2) & 1, r = quarter * 32 + lane;
+    const int pair_bar = 1 + 4 * x + quarter, mine_at = (2 * x + part) * 128 + r, other_at = (2 * x + (part ^ 1)) * 128 + r;
     const uint32_t lanes = (uint32_t)quarter * 32u << 16;
     // keys that this row sees, and that every row of the tile sees (rows that
     // belong to no token go on as if they did; nothing reads them)
-    const int lim = min(nk, i0 + r / G + 1 + shift), easy = min(nk, i0 + 1 + shift);
+    const int lim = min(nk, i0 + x * tpt + r / G + 1 + shift), easy = min(nk, i0 + x * tpt + 1 + shift), steps = steps_of(x);
     const float c = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
-      const int buf = kTwoBufs ? j & 1 : 0;
+      const int buf = kTwoBufs ? j & 1 : x;
       ok = wait(&s_full[buf], kTwoBufs ? (j >> 1) & 1 : j & 1);
       tc_fence_after();
       const uint32_t st = tmem + C::s_col(buf) + lanes + part * KH;
@@ -334,12 +382,12 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
       }
       // The maximum moves only where it grew by more than 2^8 (from -inf to
       // anything; not from -inf to -inf).
-      if (named_bar_or(1 + quarter, 64, (top - m) * c > 8.f || !ok)) {
-        exchange[part * 128 + r] = top;
-        if (lane == 0) exchange_ok[part * 4 + quarter] = ok;
-        named_bar_sync(1 + quarter, 64);
-        top = fmaxf(top, exchange[(part ^ 1) * 128 + r]);
-        ok = ok && exchange_ok[(part ^ 1) * 4 + quarter];
+      if (named_bar_or(pair_bar, 64, (top - m) * c > 8.f || !ok)) {
+        exchange[mine_at] = top;
+        if (lane == 0) exchange_ok[(2 * x + part) * 4 + quarter] = ok;
+        named_bar_sync(pair_bar, 64);
+        top = fmaxf(top, exchange[other_at]);
+        ok = ok && exchange_ok[(2 * x + (part ^ 1)) * 4 + quarter];
         if (!ok) break;
         const float was = m;
         if ((top - m) * c > 8.f) m = top;
@@ -350,7 +398,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
             ok = wait(o_done, (j - 1) & 1);
             tc_fence_after();
           }
-          const uint32_t ot = tmem + C::kO + lanes + part * DH;
+          const uint32_t ot = tmem + C::o_col(x) + lanes + part * DH;
 #pragma unroll 1
           for (int i = 0; i < DH; i += 32) {
             uint32_t o[32];
@@ -386,7 +434,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_half);
+          if (lane == 0) mbar_arrive(&p_half[buf]);
         }
       }
       l += sum.x + sum.y;
@@ -398,13 +446,13 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
     // ---- the output: the halves' sums, then rows through shared memory (Q's
     // place; no product reads it any more), 16 bytes a lane
     if (ok) {
-      named_bar_sync(1 + quarter, 64);  // (the last exchange has been read)
-      exchange[part * 128 + r] = l;
-      named_bar_sync(1 + quarter, 64);
-      l = exchange[r] + exchange[128 + r];
+      named_bar_sync(pair_bar, 64);  // (the last exchange has been read)
+      exchange[mine_at] = l;
+      named_bar_sync(pair_bar, 64);
+      l += exchange[other_at];
       // (not o_done: by now it may stand one or two products behind the last,
       // and a parity cannot tell the last but one from the one after the last)
-      if (steps > 0) ok = wait(drained, 0);
+      if (most > 0) ok = wait(drained, 0);
     }
     tc_fence_after();
     // a row that sees nothing is zero whatever its product holds
@@ -416,7 +464,7 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
     for (int i = 0; i < DH; i += 32) {
       uint32_t o[32];
       if (steps > 0 && ok) {
-        tmem_ld32(tmem + C::kO + lanes + part * DH + i, o);
+        tmem_ld32(tmem + C::o_col(x) + lanes + part * DH + i, o);
         tmem_wait_ld();
       } else {
 #pragma unroll
@@ -434,9 +482,10 @@ __global__ void __launch_bounds__(Prompt<D>::kThreads, Prompt<D>::kBlocks)
       }
     }
     __syncwarp();
-    const int group = a.h_q / a.h_kv, tok = r / group;
-    const long long mine =
-        tok < place[1] ? (long long)(place[0] + tok) * a.out_stride + (long long)(place[2] + r - tok * group) * D + part * DH : -1;
+    const int group = a.h_q / a.h_kv, rows_of_tile = 128 / group * group, tok = x * (128 / group) + r / group;
+    const long long mine = r < rows_of_tile && tok < place[1] ? (long long)(place[0] + tok) * a.out_stride +
+                                                                    (long long)(place[2] + r % group) * D + part * DH
+                                                              : -1;
 #pragma unroll 4
     for (int i = lane; i < 32 * NC; i += 32) {
       const int row = i / NC, piece = i % NC;
@@ -493,11 +542,11 @@ bool encode(CUtensorMap *map, const void *p, long long stride, int heads, int pe
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, class T>
+template <int D, class T, int NQ>
 cudaError_t launch(const PromptArgs &a, cudaStream_t stream) {
-  using C = Prompt<D>;
+  using C = Prompt<D, NQ>;
   const int G = a.h_q / a.h_kv, tpt = 128 / G;
-  const long long units = a.T_q / tpt + (long long)a.batch;
+  const long long units = a.T_q / (tpt * NQ) + (long long)a.batch;
   if (units * a.h_kv > 0x7fffffffll) return cudaErrorInvalidConfiguration;
   CUtensorMap q, k, v;
   // with no keys at all the K and V maps are never read: any rows will do
@@ -506,7 +555,7 @@ cudaError_t launch(const PromptArgs &a, cudaStream_t stream) {
       !encode<D, T>(&k, none ? a.q : a.k, none ? a.q_stride : a.k_stride, none ? a.h_q : a.h_kv, 0, none ? a.T_q : a.T_k, C::kKeys) ||
       !encode<D, T>(&v, none ? a.q : a.v, none ? a.q_stride : a.v_stride, none ? a.h_q : a.h_kv, 0, none ? a.T_q : a.T_k, C::kKeys))
     return cudaErrorInvalidValue;
-  auto *kernel = prompt_kernel<D, T>;
+  auto *kernel = prompt_kernel<D, T, NQ>;
   static std::atomic<int> allowed[kAttributeDevices];
   const cudaError_t e = allow_smem(kernel, C::kSmem, allowed);
   if (e != cudaSuccess) return e;
@@ -514,13 +563,26 @@ cudaError_t launch(const PromptArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
+template <int D, class T>
+cudaError_t launch_d(const PromptArgs &a, cudaStream_t stream) {
+  // Long sequences: two tiles share the keys' copies and operand reads, and
+  // products of 128 keys read shared memory at the rate the tensor pipe takes.
+  // Short ones: two blocks an SM hide each other's start and end.  32/8 heads,
+  // d = 128, bf16: 8192 tokens 446 us (one tile a block: 499), 4 x 2048 158 (158),
+  // 32 x 512 165 (143), 16 ragged up to 2000 272 (256); d = 64, 8192 tokens 378 (394).
+  if constexpr (D < 256) {
+    if (a.T_k > 2048ll * a.batch) return launch<D, T, 2>(a, stream);
+  }
+  return launch<D, T, 1>(a, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_prompt(const PromptArgs &a, int d, tq_dtype dt, cudaStream_t stream) {
   const bool bf = dt == TQ_BF16;
-  if (d == 64) return bf ? launch<64, __nv_bfloat16>(a, stream) : launch<64, __half>(a, stream);
-  if (d == 128) return bf ? launch<128, __nv_bfloat16>(a, stream) : launch<128, __half>(a, stream);
-  return bf ? launch<256, __nv_bfloat16>(a, stream) : launch<256, __half>(a, stream);
+  if (d == 64) return bf ? launch_d<64, __nv_bfloat16>(a, stream) : launch_d<64, __half>(a, stream);
+  if (d == 128) return bf ? launch_d<128, __nv_bfloat16>(a, stream) : launch_d<128, __half>(a, stream);
+  return bf ? launch_d<256, __nv_bfloat16>(a, stream) : launch_d<256, __half>(a, stream);
 }
 
 }  // namespace tq
