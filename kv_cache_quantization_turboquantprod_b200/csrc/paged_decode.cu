@@ -28,19 +28,23 @@
 //    x = sum_j scale_j acc_j + sum_j zero_j qsum_j, the second sum as one
 //    more product with the group sums of q in two fp16 parts.
 //  * values: A = codes of 16 channels x 16 tokens, B = p scale_j of 16 tokens
-//    x 8 heads (p's fragment transposed by movmatrix).  One more product gives
-//    sum p zero_j (A = zeros, a group a row) and sum p (A = ones, row 8).
-//    bf16 outputs take p and p scale_j in fp16 (2^-12 each against the
-//    output's own 2^-9); fp16 outputs take both in two fp16 parts (22 bits).
-// mma.sync carries them: 18 products of 16 x 8 x 16 a cell keep its tensor
-// pipe busy a third of the time that the bytes take, and the operands come
-// from registers without a trip through tensor memory.  (Queries as A with
+//    x 8 heads (p's fragment transposed by movmatrix); then, once a step, A =
+//    ones in the codes' weights, B = sums of p zero_j over four of the step's
+//    tokens, into the same accumulators: what they hold stays of the values' size.  (With sum p zero
+//    kept apart, both sums grow with the context and cancel at the end, and the
+//    tensor cores' truncating additions show: 1.7e-3 of the output at 131072
+//    tokens.)  sum p is one more product (A = ones).  bf16 outputs take p, p
+//    scale_j and p zero_j in fp16 (2^-12 each against the output's own 2^-9);
+//    fp16 outputs take them in two fp16 parts (22 bits).
+// mma.sync carries them: 18 products of 16 x 8 x 16 and 4 of half the depth a
+// cell keep its tensor pipe busy for less than half of the time that the bytes
+// take, and the operands come from registers without a trip through tensor memory.  (Queries as A with
 // idle rows 8..15 need no transposition, but their zero registers cost 60
 // moves a cell.)
 //
 // Softmax.  Weights are 2^(x - M) with a running reference M per head that
-// only has to keep p and p scale_j in fp16's range, and a bound E of the value
-// scales' exponents; both move (and the accumulators with them) when a token
+// only has to keep p, p scale_j and p zero_j in fp16's range, and a bound E of
+// the scales' and zeros' exponents; both move (and the accumulators with them) when a token
 // exceeds them, which one vote a step (two cells) finds out.
 #include "paged.cuh"
 #include "sm100.cuh"
@@ -55,7 +59,7 @@ using namespace sm100;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStep = 2;    // cells of a step
 constexpr int kStages = 2;  // steps in a warp's ring
-constexpr float kTop = 10.f, kSlack = 4.f;  // p 2^E <= 2^10 when M moves, < 2^14 always
+constexpr float kTop = 9.f, kSlack = 4.f;  // p 2^E <= 2^9 when M moves, < 2^13 always (four p zero_j stay below 2^16)
 
 __host__ __device__ constexpr int blocks_per_sm(int d) { return d == 256 ? 1 : 2; }
 
@@ -93,6 +97,13 @@ __device__ __forceinline__ void mma16_zero(float (&d)[4], uint32_t a0, uint32_t 
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// c += a b for m16n8k8.
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -102,6 +113,11 @@ __device__ __forceinline__ uint32_t pack_half2(float a, float b) { return pack2<
 __device__ __forceinline__ float2 unpack_half2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+__device__ __forceinline__ uint32_t fma_half2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b), *reinterpret_cast<__half2 *>(&c));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
@@ -398,10 +414,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     }
 
     // acc[2 j + i]: channels 32 j + 4 g + 2 i (rows g) and + 1 (rows g + 8), heads 2 t and 2 t + 1;
-    // zs: sum p zero of group g, heads 2 t and 2 t + 1, and sum p (lanes of g = 0); M: heads 2 t and 2 t + 1
-    float acc[2 * NG][4], zs[4] = {0.f, 0.f, 0.f, 0.f}, M[2] = {-kInf, -kInf};
+    // ps: sum p of heads 2 t and 2 t + 1 (every row the same); M: heads 2 t and 2 t + 1
+    float acc[2 * NG][4], ps[4] = {0.f, 0.f, 0.f, 0.f}, M[2] = {-kInf, -kInf};
     int E = -1;
-    const uint32_t ones = g == 0 ? 0x3c003c00u : 0u;
+    constexpr uint32_t kOnes = 0x3c003c00u, kOnesEven = 0x00010001u, kOnesOdd = 0x00100010u;
 #pragma unroll
     for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
@@ -484,15 +500,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
         none[ce][1] = ce * kCell + g + 8 >= valid;
       }
 
-      // ---- the reference: every scale below 2^E, every x at most M + kTop + kSlack - E
-      uint32_t top = 0;
+      // ---- the reference: every scale and zero below 2^E, every x at most M + kTop + kSlack - E
+      uint32_t top = 0;  // (a lane looks at one group of its tokens, the lanes of a t at all of them)
 #pragma unroll
-      for (int ce = 0; ce < kStep; ++ce)
-#pragma unroll
-        for (int j = 0; j < NG; j += 2) {
-          const uint4 w = *reinterpret_cast<const uint4 *>(stage + ce * C::kBytes + C::kValScale + C::scale_at(2 * t, j));
-          top = __vmaxu2(__vmaxu2(__vmaxu2(w.x, w.y), __vmaxu2(w.z, w.w)), top);
-        }
+      for (int ce = 0; ce < kStep; ++ce) {
+        const uint8_t *const at = stage + ce * C::kBytes + C::scale_at(2 * t, g % NG);
+        const uint2 sw = *reinterpret_cast<const uint2 *>(at + C::kValScale), zw = *reinterpret_cast<const uint2 *>(at + C::kValZero);
+        top = __vmaxu2(__vmaxu2(__vmaxu2(sw.x, sw.y), __vmaxu2(zw.x & 0x7fff7fffu, zw.y & 0x7fff7fffu)), top);
+      }
       top = max(top & 0xffffu, top >> 16);
       int e = (int)(top >> 10) - 14;
       float p[kStep][4], far = -kInf;  // x - M
@@ -522,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
           const float to = fmaxf(big - kTop + (float)E, M[i] + up);
           const float f = M[i] == -kInf ? 0.f : exp2f(M[i] - to);
           M[i] = to;
-          zs[i] *= f;
-          zs[i + 2] *= f;
+          ps[i] *= f;
+          ps[i + 2] *= f;
 #pragma unroll
           for (int k = 0; k < 2 * NG; ++k) {
             acc[k][i] *= f;
@@ -536,7 +551,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
         }
       }
 
-      // ---- values
+      // ---- values; zf: sums of p zero_j over the lane's tokens 2 t and 2 t + 8, and 2 t + 1 and 2 t + 9, of both cells
+      float2 zf[kTwoParts ? NG : 1];
+      uint32_t zh[kTwoParts ? 1 : NG];
 #pragma unroll
       for (int ce = 0; ce < kStep; ++ce) {
         const uint8_t *const cell = stage + ce * C::kBytes;
@@ -552,10 +569,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
             pl[o] = transpose8(pack_half2(p0 - r.x, p1 - r.y));
           }
         }
-        uint2 z = make_uint2(0u, 0u);
-        if (g < NG) z = *reinterpret_cast<const uint2 *>(cell + C::kValZero + C::scale_at(2 * t, g % NG));
-        mma16(zs, z.x, ones, z.y, ones, ph[0], ph[1]);
-        if constexpr (kTwoParts) mma16(zs, z.x, ones, z.y, ones, pl[0], pl[1]);
+        mma16(ps, kOnes, kOnes, kOnes, kOnes, ph[0], ph[1]);
+        if constexpr (kTwoParts) mma16(ps, kOnes, kOnes, kOnes, kOnes, pl[0], pl[1]);
 #pragma unroll
         for (int jp = 0; jp < NG / P; ++jp) {
           uint32_t w0[P], w1[P];
@@ -564,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
 #pragma unroll
           for (int i = 0; i < P; i += 2) {
             const uint4 sw = *reinterpret_cast<const uint4 *>(cell + C::kValScale + C::scale_at(2 * t, jp * P + i));
-            const uint32_t sc[2][2] = {{sw.x, sw.y}, {sw.z, sw.w}};
+            const uint4 zw = *reinterpret_cast<const uint4 *>(cell + C::kValZero + C::scale_at(2 * t, jp * P + i));
+            const uint32_t sc[2][2] = {{sw.x, sw.y}, {sw.z, sw.w}}, ze[2][2] = {{zw.x, zw.y}, {zw.z, zw.w}};
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int j = jp * P + i + k;
@@ -573,7 +589,11 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
               if constexpr (kTwoParts) {
                 const float2 s0 = unpack_half2(sc[k][0]), s1 = unpack_half2(sc[k][1]);
                 const float2 h0 = unpack_half2(ph[0]), h1 = unpack_half2(ph[1]), l0 = unpack_half2(pl[0]), l1 = unpack_half2(pl[1]);
-                const float y[4] = {(h0.x + l0.x) * s0.x, (h0.y + l0.y) * s0.y, (h1.x + l1.x) * s1.x, (h1.y + l1.y) * s1.y};
+                const float pt[4] = {h0.x + l0.x, h0.y + l0.y, h1.x + l1.x, h1.y + l1.y};
+                const float y[4] = {pt[0] * s0.x, pt[1] * s0.y, pt[2] * s1.x, pt[3] * s1.y};
+                const float2 z0 = unpack_half2(ze[k][0]), z1 = unpack_half2(ze[k][1]);
+                zf[j].x = fmaf(pt[0], z0.x, fmaf(pt[2], z1.x, ce ? zf[j].x : 0.f));
+                zf[j].y = fmaf(pt[1], z0.y, fmaf(pt[3], z1.y, ce ? zf[j].y : 0.f));
                 b0 = pack_half2(y[0], y[1]);
                 b1 = pack_half2(y[2], y[3]);
                 const float2 r0 = unpack_half2(b0), r1 = unpack_half2(b1);
@@ -583,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
               } else {
                 b0 = mul_half2(ph[0], sc[k][0]);
                 b1 = mul_half2(ph[1], sc[k][1]);
+                zh[j] = fma_half2(ph[1], ze[k][1], ce ? fma_half2(ph[0], ze[k][0], zh[j]) : mul_half2(ph[0], ze[k][0]));
               }
               mma16(acc[2 * j], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
               mma16(acc[2 * j + 1], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, b0, b1);
@@ -590,11 +611,25 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
           }
         }
       }
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        if constexpr (kTwoParts) {
+          // high and low part in the two halves of k
+          const uint32_t h = pack_half2(zf[j].x, zf[j].y);
+          const float2 r = unpack_half2(h);
+          const uint32_t lo = pack_half2(zf[j].x - r.x, zf[j].y - r.y);
+          mma16(acc[2 * j], kOnesEven, kOnesOdd, kOnesEven, kOnesOdd, h, lo);
+          mma16(acc[2 * j + 1], kOnesEven, kOnesOdd, kOnesEven, kOnesOdd, h, lo);
+        } else {
+          mma8(acc[2 * j], kOnesEven, kOnesOdd, zh[j]);
+          mma8(acc[2 * j + 1], kOnesEven, kOnesOdd, zh[j]);
+        }
+      }
     }
 
     // ---- a unit that is all here goes to the output, the rest to a record
     if (bad && lane == 0) atomicOr(a.c.errors, TQ_ERRF_PAGE);
-    if (bad || dead) zs[2] = zs[3] = __int_as_float(0x7fffffff);
+    if (bad || dead) ps[0] = ps[1] = __int_as_float(0x7fffffff);
     const int ends = (here.step == 0 ? 1 : 0) | (here.step + end - at == here.steps ? 2 : 0);
     const int slot = 2 * warp + (at == begin ? 0 : 1);
     // the last record lies in the warp's own ring, whose copies have all been used
@@ -607,24 +642,22 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
         for (int i = 0; i < 2; ++i)
           if (2 * t + i < G) {
             rec_state[2 * (2 * t + i)] = M[i];
-            rec_state[2 * (2 * t + i) + 1] = zs[2 + i];
+            rec_state[2 * (2 * t + i) + 1] = ps[i];
           }
       if (lane == 0) info[slot] = Record{here.b, here.h, ends, at};
     }
-    const float sum[2] = {__shfl_sync(0xffffffffu, zs[2], t), __shfl_sync(0xffffffffu, zs[3], t)};
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
-      const float z[2] = {__shfl_sync(0xffffffffu, zs[0], 4 * j + t), __shfl_sync(0xffffffffu, zs[1], 4 * j + t)};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float w = 16777216.f;
         if (2 * t + i < G) {
-          const float4 o = make_float4(fmaf(acc[2 * j][i], w, z[i]), fmaf(acc[2 * j][i + 2], w * 0.0625f, z[i]),
-                                       fmaf(acc[2 * j + 1][i], w, z[i]), fmaf(acc[2 * j + 1][i + 2], w * 0.0625f, z[i]));
+          const float4 o = make_float4(acc[2 * j][i] * w, acc[2 * j][i + 2] * (w * 0.0625f), acc[2 * j + 1][i] * w,
+                                       acc[2 * j + 1][i + 2] * (w * 0.0625f));
           if (ends != 3) {
             *reinterpret_cast<float4 *>(rec + (2 * t + i) * D + 32 * j + 4 * g) = o;
           } else {
-            const float r = 1.f / sum[i];
+            const float r = 1.f / ps[i];
             T *out = reinterpret_cast<T *>(a.out) + (size_t)here.b * a.out_stride + (size_t)(here.h * G + 2 * t + i) * D;
             *reinterpret_cast<uint2 *>(out + 32 * j + 4 * g) = make_uint2(pack2<T>(o.x * r, o.y * r), pack2<T>(o.z * r, o.w * r));
           }

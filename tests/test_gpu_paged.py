@@ -54,6 +54,16 @@ def _tolerance(out, spread, biggest, d, dtype, p_dtype):
     return torch.finfo(dtype).eps / 2 * np.abs(out) + (torch.finfo(p_dtype).eps / 2 + 2 * logit) * spread + 1e-7
 
 
+def _decode_tolerance(out, spread, largest, biggest, d, dtype):
+    """_tolerance, with the roundings of the cached values' two terms in the place of the probabilities' own: p scale code and
+    p zero are formed apart, of sizes that add up to at most spread + 2 max |v| (zero is a group's smallest value, scale code
+    what lies above it).  bf16 outputs: p, p scale, and the sums of four p zero are fp16 (2^-11 each, at most five in a row).
+    fp16 outputs: two fp16 parts each (2^-22), the same number of times, and additions that truncate (2^-23, sixteen a product
+    and two products)."""
+    r = 5 * 2.0 ** -11 if dtype == BF16 else 5 * 2.0 ** -22 + 32 * 2.0 ** -23
+    return _tolerance(out, spread, biggest, d, dtype, F32) + r * (spread + 2 * largest)
+
+
 class Setup:
     """A pool filled with a byte pattern, its oracle twin, and sequences of given total lengths."""
 
@@ -219,9 +229,7 @@ def _check_decode(st, kv, q, out, scale, lens=None):
         for hq in range(q.shape[1]):
             k, v = kv[b, hq // G]
             o, spread, big = paged.attend(qs[b, hq], k, v, n, scale)
-            # value codes up to 15 scales above zero meet the rounded probabilities: their size, not the values'
-            room = spread + (np.abs(v[:n]).max(0) * 2 if n else 0)
-            tol = _tolerance(o, room, big, d, dt, F16)
+            tol = _decode_tolerance(o, spread, np.abs(v[:n]).max() if n else 0.0, big, d, dt)
             assert (np.abs(got[b, hq] - o) <= tol).all(), (b, hq, np.abs(got[b, hq] - o).max())
 
 
@@ -295,8 +303,8 @@ def test_decode_long_and_ragged():
         w = torch.softmax(s, -1)
         o, spread = w @ vb, w @ vb.abs()
         big = float((q[b].double().abs().view(h_kv, -1, d) @ kb.abs().transpose(1, 2)).max() * d ** -0.5)
-        tol = _tolerance(_np(o), _np(spread), big, d, F16, F16)
-        assert (np.abs(_np(out[b].view(h_kv, -1, d)) - _np(o)) <= 3 * tol).all()
+        tol = _decode_tolerance(_np(o), _np(spread), float(vb.abs().max()), big, d, F16)
+        assert (np.abs(_np(out[b].view(h_kv, -1, d)) - _np(o)) <= tol).all()
         at += n
 
 
@@ -337,7 +345,7 @@ def test_pool_beyond_four_gigabytes():
     tq.tq_paged_decode_attention(cache, batch, q, out, tq.paged_workspace_for(cache, batch, 16))
     for hq in range(16):
         o, spread, big = paged.attend(_np(q)[0, hq], _np(kc)[:, hq // 2], _np(vc)[:, hq // 2], n, d ** -0.5)
-        tol = _tolerance(o, spread + 2 * np.abs(_np(vc)[:, hq // 2]).max(0), big, d, BF16, F16)
+        tol = _decode_tolerance(o, spread, np.abs(_np(vc)[:, hq // 2]).max(), big, d, BF16)
         assert (np.abs(_np(out)[0, hq] - o) <= tol).all()
 
 
@@ -515,7 +523,7 @@ def test_a_serving_run(d, h_q, h_kv, dtype, page):
                 for hq in range(h_q):
                     kk, vv = _np(k)[at : at + m, hq * h_kv // h_q], _np(v)[at : at + m, hq * h_kv // h_q]
                     o, spread, big = paged.attend(_np(q)[b, hq], kk, vv, m, d ** -0.5)
-                    tol = _tolerance(o, spread + 2 * np.abs(vv).max(0), big, d, dtype, F16)
+                    tol = _decode_tolerance(o, spread, np.abs(vv).max(), big, d, dtype)
                     assert (np.abs(_np(out)[b, hq] - o) <= tol).all()
                 at += m
 
