@@ -662,10 +662,10 @@ TQ_API tq_status tq_paged_decode_attention(const tq_paged_cache *c, const tq_pag
  *                  and T_k (values outside are clamped); the same array may
  *                  serve both
  * Rows of q at or behind cu_q[batch] are ignored and their rows of out are
- * left as they are.  Keys and values of other sequences and those behind
- * cu_k[batch] never reach a result, whatever they hold.  Within a sequence a
- * NaN or an infinity in the value row of a key may also reach queries up to
- * 127 positions before it.
+ * left as they are.  What a query does not see (later keys of its sequence,
+ * other sequences, rows behind cu_k[batch]) never reaches its result, whatever
+ * it holds.  A query that sees an infinity in a value row may get NaN in its
+ * place.
  */
 TQ_API tq_status tq_prompt_attention(const void *q, const void *k, const void *v, tq_dtype dtype, int T_q, int T_k,
                                      int h_q, int h_kv, int d, long long q_stride, long long k_stride,

@@ -32,9 +32,11 @@
 // descriptor.
 //
 // Masked scores are replaced, not added to, so what K holds there does not
-// matter; V rows that no row of the block sees (another sequence's, or
-// padding) are cleared in shared memory by warp 2 before they are used, since
-// 0 x NaN is NaN.
+// matter.  0 x NaN is NaN, so V is looked at before it is used wherever a row
+// of the block does not see a key of the step (the last steps): warps 2 and 3
+// clear the rows that nothing sees (another sequence's, or padding), and
+// replace infinities and NaN by 0, noting for each channel the first key that
+// had one; at the end the rows that see that key get NaN there.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -66,8 +68,9 @@ struct Prompt {
   static constexpr int kStages = D == 64 ? 8 : D == 128 ? (NQ == 2 ? 5 : 4) : 5;
   static constexpr int kThreads = 128 + 256 * NQ;
   static constexpr int kExchange = NQ * kQTile + kStages * kStage;  // [NQ][2][128] floats, [NQ][2][4] ints
-  static constexpr int kBars = kExchange + NQ * (1024 + 32);
-  static constexpr size_t kSmem = kBars + 256;
+  static constexpr int kBad = kExchange + NQ * (1024 + 32);  // [D] ints: the first key with a special value
+  static constexpr int kBars = kBad + D * 4;
+  static constexpr size_t kSmem = kBars + 384;
   // tensor memory columns: S (and P over it) of buffer or tile x, O of tile x
   static constexpr uint32_t kColumns = kBlocks == 2 ? 256 : 512;
   __host__ __device__ static constexpr uint32_t s_col(int x) { return (uint32_t)kKeys * x; }
@@ -127,15 +130,16 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
   extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms)
   uint8_t *const stages = smem + NQ * C::kQTile;
   float *const exchange = reinterpret_cast<float *>(smem + C::kExchange);
-  int *const exchange_ok = reinterpret_cast<int *>(exchange + NQ * 256);
+  int *const exchange_ok = reinterpret_cast<int *>(exchange + NQ * 256), *const bad = reinterpret_cast<int *>(smem + C::kBad);
   uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + C::kBars);
   // [2]: by buffer (NQ = 1) or by tile
   uint64_t *const q_full = bars, *const kv_full = bars + 1, *const kv_empty = kv_full + ST, *const s_full = kv_empty + ST,
                   *const p_ready = s_full + 2, *const p_half = p_ready + 2, *const o_done = p_half + 2,
-                  *const v_last = o_done + 1, *const v_clear = v_last + 1, *const drained = v_clear + 1;
+                  *const v_here = o_done + 1, *const v_clear = v_here + ST, *const drained = v_clear + ST;
   uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  // the block's first row and its tokens, for the end (out of the registers until then)
+  // the block's first row, its tokens and first head, for the end (out of the registers until then); [3]: V had
+  // special values
   volatile int *const place = abort_flag + 1;
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -154,13 +158,16 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
   auto keys_of = [&](int x) { return i0 + x * tpt < nq ? max(min(nk, min(nq, i0 + (x + 1) * tpt) + shift), 0) : 0; };
   auto steps_of = [&](int x) { return (keys_of(x) + KT - 1) / KT; };
   const int seen = max(keys_of(0), NQ == 2 ? keys_of(1) : 0), most = (seen + KT - 1) / KT;
-  const bool clears = seen < most * KT;  // the last V tile has rows that nothing sees
+  // the first step with a key that some row does not see: V is looked at from there on
+  const int looked = max(min(min(nk, i0 + 1 + shift), seen), 0) / KT;
 
   if (warp == 0 && lane == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < ST; ++s) {
       mbar_init(&kv_full[s], 1);
       mbar_init(&kv_empty[s], 1);
+      mbar_init(&v_here[s], 1);
+      mbar_init(&v_clear[s], 2);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
@@ -168,15 +175,15 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       mbar_init(&p_half[x], 8);
     }
     mbar_init(o_done, 1);
-    mbar_init(v_last, 1);
-    mbar_init(v_clear, 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     place[0] = q0 + i0;
     place[1] = min(nq - i0, tb);
     place[2] = h * G;
+    place[3] = 0;
     fence_mbar_init();
   }
+  for (int i = tid; i < D; i += C::kThreads) bad[i] = 0x7fffffff;
   if (warp == 1) {
     tmem_alloc(tmem_slot, C::kColumns);
     tmem_relinquish();
@@ -191,6 +198,9 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, pipe_wait(bar, parity, abort_flag, a.wait_ns, hint, &timed_out));
   };
+
+  // which use of its stage among the steps that are looked at V of step j is: V's place comes round every so many steps
+  auto use_of = [&](int j) { return (uint32_t)((j - looked) / (ST % 2 ? ST : ST / 2)) & 1u; };
 
   if (warp < 4) {
     reg_dealloc<C::kFew>();
@@ -209,6 +219,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
           for (int s = 0; s < C::kSlabs; ++s)
             tma_load_3d(stages + st * C::kStage + s * C::kSlab, item & 1 ? &vmap : &kmap, 64 * s, h, k0 + (item >> 1) * KT,
                         &kv_full[st]);
+          if ((item & 1) && item >> 1 >= looked) mbar_arrive(&v_here[st]);
         }
         // shared memory is the block's until its own copies have landed
         mbar_wait(q_full, 0);
@@ -259,10 +270,10 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
         p.advance();
       };
       auto landed = [&](const Place &p) { return wait(&kv_full[p.st], p.phase); };
-      // the last V tile goes to warp 2 first
-      auto cleared = [&] {
-        if (lane == 0) mbar_arrive(v_last);
-        return wait(v_clear, 0);
+      // V of step j is here, and looked at
+      auto value_tile = [&](int j) {
+        if (!landed(vp)) return false;
+        return j < looked || wait(&v_clear[vp.st], use_of(j));
       };
       bool ok = most == 0 || (wait(q_full, 0) && landed(kp));
       tc_fence_after();
@@ -281,7 +292,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
             scores(0, (j + 1) & 1);
             release(kp);
           }
-          ok = landed(vp) && (!clears || j + 1 < most || cleared()) && wait(&p_ready[j & 1], (j >> 1) & 1);
+          ok = value_tile(j) && wait(&p_ready[j & 1], (j >> 1) & 1);
           tc_fence_after();
           if (!ok) break;
           values(0, j & 1, j, 2);
@@ -292,7 +303,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
         for (int j = 0; ok && j < most; ++j) {
           // (each tile is asked for just before its first use and given back just
           // after its last, or the copies do not come in time)
-          ok = landed(vp) && (!clears || j + 1 < most || cleared());
+          ok = value_tile(j);
           bool next = false;  // K(j + 1) is here
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
@@ -321,17 +332,48 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       if (leader) mma_commit(drained);
       __syncwarp();
       mbar_wait(drained, 0);
-    } else if (warp == 2 && clears && most > 0) {
-      // ---- V rows that nothing sees
-      const int item = 2 * most - 1, rows = most * KT - seen;
-      if (wait(v_last, 0)) {
-        uint8_t *v = stages + (item % ST) * C::kStage + (KT - rows) * 128;
-        for (int i = lane; i < rows * 8; i += 32)
+    } else {
+      // ---- the look at V.  (The loader tells of a copy when it issues it: until
+      // then the stage's barrier may stand a phase behind, which a parity does
+      // not tell from the phase after.)
+      constexpr uint32_t field = kBf16 ? 0x7f807f80u : 0x7c007c00u, one = kBf16 ? 0x00800080u : 0x04000400u;
+      constexpr int kUnits = C::kStage / 16 / 64, kBatch = 8;  // 16-byte pieces of a lane
+      static_assert(kUnits % kBatch == 0, "whole batches");
+      for (int j = looked; j < most; ++j) {
+        const int st = (2 * j + 1) % ST;
+        if (!wait(&v_here[st], use_of(j)) || !wait(&kv_full[st], (2 * j + 1) / ST & 1)) break;
+        uint4 *const v = reinterpret_cast<uint4 *>(stages + st * C::kStage);
+        const int rows = seen - j * KT, first = (warp - 2) * 32 + lane;  // rows that something sees
+        if (rows < KT)
+          for (int i = first; i < 64 * kUnits; i += 64)
+            if (i / 8 % KT >= rows) v[i] = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int i0 = 0; i0 < kUnits; i0 += kBatch) {
+          uint32_t any = 0;
+          uint4 u[kBatch];
 #pragma unroll
-          for (int s = 0; s < C::kSlabs; ++s) *reinterpret_cast<uint4 *>(v + s * C::kSlab + i * 16) = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < kBatch; ++k) u[k] = v[first + 64 * (i0 + k)];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k)
+            any |= ((u[k].x & field) + one) | ((u[k].y & field) + one) | ((u[k].z & field) + one) | ((u[k].w & field) + one);
+          if (any & 0x80008000u) {
+#pragma unroll 1
+            for (int k = 0; k < kBatch; ++k) {
+              const int i = first + 64 * (i0 + k), row = i / 8 % KT, channel = i / (8 * KT) * 64 + (i % 8 ^ (row & 7)) * 8;
+              uint16_t *const at = reinterpret_cast<uint16_t *>(v + i);
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e)
+                if ((at[e] & field & 0xffffu) == (field & 0xffffu)) {
+                  at[e] = 0;
+                  atomicMin(&bad[channel + e], j * KT + row);
+                  place[3] = 1;
+                }
+            }
+          }
+        }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(v_clear);
+        if (lane == 0) mbar_arrive(&v_clear[st]);
       }
     }
   } else {
@@ -458,6 +500,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
     // a row that sees nothing is zero whatever its product holds
     const bool none = ok && lim <= 0;
     const float w = !ok ? __int_as_float(0x7fffffff) : 1.f / l;
+    const bool special = place[3] != 0;
     constexpr int NC = DH / 8;  // 16-byte pieces of a row's half
     uint8_t *const rows = smem + (warp - 4) * 32 * NC * 16;
 #pragma unroll
@@ -469,6 +512,11 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0;
+      }
+      if (special) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (bad[part * DH + i + e] < lim) o[e] = 0x7fffffffu;
       }
 #pragma unroll
       for (int e = 0; e < 32; e += 8) {

@@ -444,6 +444,37 @@ def test_prompt_scales_and_infinite_neighbours(d, h_q, h_kv, softmax):
     _check_prompt(q[:59], k[:59], v[:59], [59], [59], out[:59], softmax)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d,h_q,h_kv", [(128, 8, 2), (64, 3, 3), (256, 6, 1), (128, 4, 4)])
+@pytest.mark.parametrize("long", [False, True])
+def test_prompt_special_values_reach_only_who_sees_them(d, h_q, h_kv, dtype, long):
+    """A NaN or an infinity in one channel of a value row: NaN or that infinity for the queries from its token on, in that
+    channel alone; a NaN key row: NaN for those queries; nothing for earlier ones."""
+    n = 2300 if long else 210  # one tile a block, and two
+    q, k, v = _prompt_inputs(d, h_q, h_kv, dtype, [n], [n], seed=8, pad=0)
+    cu = _cu([n])
+    clean = torch.zeros_like(q, device=DEV)
+    tq.tq_prompt_attention(q.to(DEV), k.to(DEV), v.to(DEV), cu, cu, clean)
+    hit = {n - 150: 3, n - 149: d - 1, n - 64: 17, n - 1: 0}
+    bad = v.clone()
+    for (t, c), x in zip(hit.items(), (float("nan"), float("inf"), float("-inf"), float("nan"))):
+        bad[t, 0, c] = x
+    out = torch.zeros_like(clean)
+    tq.tq_prompt_attention(q.to(DEV), k.to(DEV), bad.to(DEV), cu, cu, out)
+    want = torch.ones(n, h_q, d, dtype=torch.bool, device=DEV)
+    for t, c in hit.items():
+        want[t:, : h_q // h_kv, c] = False
+    assert torch.equal(torch.isfinite(out), want)
+    assert torch.equal(out[want], clean[want])
+    bad = k.clone()
+    bad[n - 70, 0, 5] = float("nan")
+    tq.tq_prompt_attention(q.to(DEV), bad.to(DEV), v.to(DEV), cu, cu, out)
+    want[:] = True
+    want[n - 70 :, : h_q // h_kv] = False
+    assert torch.equal(torch.isfinite(out), want)
+    assert torch.equal(out[want], clean[want])
+
+
 def test_prompt_long_against_float64_on_device():
     d, h_q, h_kv, new, past = 128, 8, 2, (2000, 3, 1111), (0, 3000, 517)
     nk = [a + b for a, b in zip(new, past)]
