@@ -430,8 +430,8 @@ TQ_API tq_status tq_set_wait_limit_ns(unsigned long long ns);
 /*
  * tq_test_withhold_handoffs -- for tests of the timeout path only: while on
  * (nonzero), the tensor-core kernels of later calls withhold one hand-off
- * that their other roles wait for (decode: the tile copies; quantize-append:
- * the loaded key operand), so those bounded waits run out after the wait
+ * that their other roles wait for (decode, paged decode, paged append and
+ * prompt: their copies; quantize-append: the loaded key operand), so those bounded waits run out after the wait
  * limit and the failure reporting above can be observed.  Nothing faults:
  * every wait is bounded and each kernel returns.  Off by default.  Always
  * TQ_OK.
@@ -504,7 +504,7 @@ TQ_API tq_status tq_dequantize(const tq_params *p, const tq_cache *c, int b,
  * range (65504) are not representable.
  * ------------------------------------------------------------------------ */
 
-/* Largest query heads per KV head of the paged decode and the prompt call. */
+/* Largest number of query heads per KV head of the paged and prompt calls. */
 #define TQ_PAGED_MAX_GQA 8
 
 /*
@@ -596,7 +596,9 @@ TQ_API size_t tq_paged_bytes(int d, int h_kv, int page_tokens, int num_pages);
  * each; two sequences that name the same page must not append to it.
  * Errors: TQ_ERR_INVALID_ARGUMENT (null or misaligned pointers, negative
  * sizes, h_q not a multiple of h_kv, q without q_out), TQ_ERR_UNSUPPORTED (d,
- * page_tokens, rotary_dim, dtype).
+ * page_tokens, rotary_dim, dtype, more than TQ_PAGED_MAX_GQA query heads a KV
+ * head), TQ_ERR_CAPACITY (more than 2^30 tokens or positions).  A kernel whose
+ * bounded wait runs out sets TQ_ERRF_QUANTIZE_WAIT and leaves tokens unwritten.
  */
 TQ_API tq_status tq_paged_append(const tq_paged_cache *c, const tq_paged_batch *s, const tq_rope *rope,
                                  const int32_t *cu_new, const void *q, const void *k, const void *v, tq_dtype dtype,
@@ -639,7 +641,10 @@ TQ_API size_t tq_paged_decode_workspace_size(const tq_paged_cache *c, int batch,
  *   workspace  device, tq_paged_decode_workspace_size() bytes, 256-byte
  *              aligned, no initialisation; one per call in flight
  * A sequence with no tokens gets a zero row, one with a bad page NaN rows.
- * Lengths beyond max_pages * page_tokens are bad pages.
+ * Lengths beyond max_pages * page_tokens are bad pages.  softmax_scale times
+ * log2(e) must be finite; logits beyond 2^24, which float32 does not resolve
+ * to a softmax, may give NaN.  A kernel whose bounded wait runs out writes NaN
+ * rows and sets TQ_ERRF_DECODE_WAIT.
  */
 TQ_API tq_status tq_paged_decode_attention(const tq_paged_cache *c, const tq_paged_batch *s, const void *q,
                                            tq_dtype dtype, int h_q, long long q_stride, float softmax_scale, void *out,
@@ -665,7 +670,9 @@ TQ_API tq_status tq_paged_decode_attention(const tq_paged_cache *c, const tq_pag
  * left as they are.  What a query does not see (later keys of its sequence,
  * other sequences, rows behind cu_k[batch]) never reaches its result, whatever
  * it holds.  A query that sees an infinity in a value row may get NaN in its
- * place.
+ * place.  softmax_scale and large logits as for tq_paged_decode_attention.  A
+ * kernel whose bounded wait runs out writes NaN rows and sets
+ * TQ_ERRF_PROMPT_WAIT.
  */
 TQ_API tq_status tq_prompt_attention(const void *q, const void *k, const void *v, tq_dtype dtype, int T_q, int T_k,
                                      int h_q, int h_kv, int d, long long q_stride, long long k_stride,

@@ -21,6 +21,8 @@ struct PagedView {
   int page_shift;  // log2 of the tokens of a page
   int num_pages, h_kv;
   unsigned int *errors;
+  unsigned long long wait_ns;  // limit of the bounded waits
+  int withhold;                // tests of the timeout path: no copies
 };
 
 // Sections and strides of a cell of head dim D (bytes).
@@ -48,6 +50,9 @@ struct Cell {
   }
   __host__ __device__ static constexpr int key_zero_at(int n, int j) { return (n * kGroups + j) * 2; }
 };
+
+// Lengths and first positions beyond any table's row, without overflow.
+__device__ __forceinline__ int clamp_position(int x) { return min(max(x, -(1 << 30)), 1 << 30); }
 
 // The page of position pos of sequence b; -1 where the table has none.
 __device__ __forceinline__ int page_of(const PagedView &c, int b, int pos) {
@@ -184,6 +189,7 @@ struct PromptArgs {
   float scale_log2;  // |softmax scale| times log2(e), at least 1e-30
   int negate;        // the scale is negative
   unsigned long long wait_ns;
+  int withhold;
   unsigned int *errors;
 };
 cudaError_t launch_prompt(const PromptArgs &a, int d, tq_dtype dt, cudaStream_t stream);

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) paged_append_kernel(con
   const int h = blockIdx.x % a.c.h_kv, u = blockIdx.x / a.c.h_kv;
   const int b = unit_sequence<4>(a.cu, a.c.batch, a.T, u);
   const int r0 = clamp_cu(a.cu, b, a.T), r1 = max(clamp_cu(a.cu, b + 1, a.T), r0);
-  const int first = a.c.len[b] - (r1 - r0);  // position of row r0
+  const int first = clamp_position(a.c.len[b]) - (r1 - r0);  // position of row r0
   const int cell = (first >> 4) + u - ((r0 >> 4) + 2 * b);
   // rows of this cell: positions 16 cell .. 16 cell + 15
   const int lo = max(16 * cell, first), hi = min(16 * cell + 16, first + (r1 - r0));
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) paged_append_kernel(con
   const int from = max(own, lo), count = max(min(own + kOwn, hi) - from, 0);
   __syncwarp();
   if (lane == 0 && count > 0) sm100::mbar_arrive_expect_tx(bar, (uint32_t)(count * row_elems * sizeof(T)));
-  if (lane < 3 * count) {
+  if (lane < 3 * count && !a.c.withhold) {
     const int pos = from + lane / 3, kind = lane % 3;
     T *const to = rows + (pos - 16 * cell) * row_elems;
     const size_t row = (size_t)(r0 + (pos - first));
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) paged_append_kernel(con
   if (page < 0 && tid == 0) atomicOr(a.c.errors, TQ_ERRF_PAGE);
   if (live && !in_table && p == 0 && h == 0) atomicOr(a.c.errors, TQ_ERRF_POSITION);
   // (a copy always lands; should a wait run out, the warp's rows stay unwritten)
-  const bool ok = count > 0 && __all_sync(0xffffffffu, sm100::mbar_wait(bar, 0));
+  const bool ok = count > 0 && __all_sync(0xffffffffu, sm100::mbar_wait(bar, 0, a.c.wait_ns));
   if (count > 0 && !ok && lane == 0) atomicOr(a.c.errors, TQ_ERRF_QUANTIZE_WAIT);
 
   if (ok) {

@@ -203,8 +203,7 @@ struct Cursor {
 };
 
 template <int D, class T>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a,
-                                                                                  unsigned long long wait_ns) {
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
   using C = Cell<D>;
   using S = Smem<D>;
   constexpr int NG = C::kGroups, P = C::kP;
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     const int s = asked % kStages, first = kStep * next.step, have = min(cells - first, kStep);
     const bool bad = (uint32_t)page0 >= (uint32_t)a.c.num_pages || (!joined && (uint32_t)page1 >= (uint32_t)a.c.num_pages);
     bad_stage = (bad_stage & ~(1u << s)) | ((uint32_t)bad << s);
-    if (lane == 0) {
+    if (lane == 0 && !a.c.withhold) {
       uint8_t *const to = ring + s * S::kStage;
       const uint8_t *const from = a.c.data + (size_t)page0 * page_bytes + (size_t)next.h * head_bytes;
       if (bad) {
@@ -427,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       __syncwarp();
       issue();
       const int s = used % kStages;
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], (used / kStages) & 1, wait_ns))) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], (used / kStages) & 1, a.c.wait_ns))) {
         dead = true;
         if (lane == 0) atomicOr(a.c.errors, TQ_ERRF_DECODE_WAIT);
         break;
@@ -669,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     if (at < stop) here.settle(a.c);
   }
   // a warp that gave up still waits for its own copies
-  if (dead)
+  if (dead && !a.c.withhold)
     for (int i = used; i < asked; ++i) mbar_wait(&bars[i % kStages], (i / kStages) & 1);
 
   // ---- the block joins its warps' records: runs of one unit, in order
@@ -794,7 +793,7 @@ cudaError_t launch(const PagedDecodeArgs &a, cudaStream_t stream) {
   static std::atomic<int> allowed[kAttributeDevices];
   cudaError_t e = allow_smem(kernel, Smem<D>::bytes(TQ_PAGED_MAX_GQA), allowed);
   if (e != cudaSuccess) return e;
-  kernel<<<blocks, kThreads, smem, stream>>>(a, wait_limit_ns());
+  kernel<<<blocks, kThreads, smem, stream>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_combine_kernel<D, T>, dim3(a.c.batch * a.h_q), dim3(128), 0, stream, a, blocks);

@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(32 * kWarps) paged_gather_kernel(const __grid_
   if (u >= span_units<4>(a.rows, a.c.batch)) return;
   const int b = unit_sequence<4>(a.cu, a.c.batch, a.rows, (int)u);
   const int r0 = clamp_cu(a.cu, b, a.rows), r1 = max(clamp_cu(a.cu, b + 1, a.rows), r0);
-  const int first = a.first ? a.first[b] : 0;
+  const int first = a.first ? clamp_position(a.first[b]) : 0;
   const int cell = (first >> 4) + (int)u - ((r0 >> 4) + 2 * b);
   const int lo = max(16 * cell, first), hi = min(16 * cell + 16, first + (r1 - r0));
   if (lo >= hi) return;

@@ -2,7 +2,6 @@
 // (include/tq.h): host-side validation and launches.  Nothing here allocates
 // or synchronises.
 #include <cmath>
-#include <vector>
 
 #include "paged.cuh"
 #include "tq_kernels.h"
@@ -47,12 +46,14 @@ tq_status view(const tq_paged_cache *c, const tq_paged_batch *s, tq::PagedView *
   while ((1 << v->page_shift) < c->page_tokens) ++v->page_shift;
   v->num_pages = c->num_pages;
   v->h_kv = c->h_kv;
+  v->wait_ns = tq::wait_limit_ns();
+  v->withhold = tq::handoffs_withheld();
   return tq::device_error_word(&v->errors) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 tq_status check_heads(int h_q, int h_kv) {
   if (h_kv < 1 || h_q < h_kv || h_q % h_kv) return TQ_ERR_INVALID_ARGUMENT;
-  return TQ_OK;
+  return h_q / h_kv > TQ_PAGED_MAX_GQA ? TQ_ERR_UNSUPPORTED : TQ_OK;
 }
 
 tq_status done(cudaError_t e) { return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA; }
@@ -146,7 +147,6 @@ tq_status tq_paged_gather(const tq_paged_cache *c, const tq_paged_batch *s, cons
 
 size_t tq_paged_decode_workspace_size(const tq_paged_cache *c, int batch, int h_q) {
   if (check_cache(c) != TQ_OK || batch < 1 || check_heads(h_q, c->h_kv) != TQ_OK) return 0;
-  if (h_q / c->h_kv > TQ_PAGED_MAX_GQA) return 0;
   int sms = 0;
   if (tq::device_sm_count(&sms) != cudaSuccess) return 0;
   return tq::paged_decode_workspace(c->d, c->h_kv, h_q, batch, sms);
@@ -160,8 +160,7 @@ tq_status tq_paged_decode_attention(const tq_paged_cache *c, const tq_paged_batc
   if ((st = check_batch(c, s)) != TQ_OK) return st;
   if (dtype != TQ_BF16 && dtype != TQ_F16) return TQ_ERR_UNSUPPORTED;
   if ((st = check_heads(h_q, c->h_kv)) != TQ_OK) return st;
-  if (h_q / c->h_kv > TQ_PAGED_MAX_GQA) return TQ_ERR_UNSUPPORTED;
-  if (!std::isfinite(softmax_scale)) return TQ_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(softmax_scale * kLog2e)) return TQ_ERR_INVALID_ARGUMENT;
   const long long row = (long long)h_q * c->d;
   if (!rows_ok(q, q_stride, row, dtype) || !rows_ok(out, out_stride, row, dtype)) return TQ_ERR_INVALID_ARGUMENT;
   if ((long long)s->batch * h_q > 0x7fffffffll) return TQ_ERR_CAPACITY;
@@ -184,11 +183,10 @@ tq_status tq_prompt_attention(const void *q, const void *k, const void *v, tq_dt
   if (dtype != TQ_BF16 && dtype != TQ_F16) return TQ_ERR_UNSUPPORTED;
   tq_status st = check_heads(h_q, h_kv);
   if (st != TQ_OK) return st;
-  if (h_q / h_kv > TQ_PAGED_MAX_GQA) return TQ_ERR_UNSUPPORTED;
   if (T_q < 0 || T_k < 0 || batch < 1 || !cu_q || !cu_k || !aligned(cu_q, 4) || !aligned(cu_k, 4))
     return TQ_ERR_INVALID_ARGUMENT;
   if (batch > (1 << 20) || T_q > (1 << 30) || T_k > (1 << 30)) return TQ_ERR_CAPACITY;
-  if (!std::isfinite(softmax_scale)) return TQ_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(softmax_scale * kLog2e)) return TQ_ERR_INVALID_ARGUMENT;
   if (T_q == 0) return TQ_OK;
   const long long qrow = (long long)h_q * d, row = (long long)h_kv * d;
   if (!rows_ok(q, q_stride, qrow, dtype) || !rows_ok(out, out_stride, qrow, dtype)) return TQ_ERR_INVALID_ARGUMENT;
@@ -203,6 +201,7 @@ tq_status tq_prompt_attention(const void *q, const void *k, const void *v, tq_dt
   a.scale_log2 = std::fmax(std::fabs(softmax_scale) * kLog2e, 1e-30f);
   a.negate = softmax_scale < 0.f;
   a.wait_ns = tq::wait_limit_ns();
+  a.withhold = tq::handoffs_withheld();
   if (tq::device_error_word(&a.errors) != cudaSuccess) return TQ_ERR_CUDA;
   return done(tq::launch_prompt(a, d, dtype, (cudaStream_t)stream));
 }

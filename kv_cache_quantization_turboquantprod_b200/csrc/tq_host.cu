@@ -354,6 +354,7 @@ namespace tq {
 cudaError_t device_sm_count(int *out) { return current_sm_count(out); }
 cudaError_t device_error_word(unsigned int **out) { return error_word_address(out); }
 unsigned long long wait_limit_ns() { return g_wait_ns.load(std::memory_order_relaxed); }
+int handoffs_withheld() { return g_withhold.load(std::memory_order_relaxed); }
 
 // Shared by tq_decode_attention, tq_decode_attention_window (win_k null: no
 // window) and tq_decode_attention_noalloc (the library's scratch as workspace).

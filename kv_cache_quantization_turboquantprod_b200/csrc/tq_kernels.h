@@ -208,7 +208,9 @@ cudaError_t launch_dequantize(const DequantArgs &a, cudaStream_t stream);
 // word (both cached per device).
 cudaError_t device_sm_count(int *out);
 cudaError_t device_error_word(unsigned int **out);
-// The bounded waits' limit (tq_set_wait_limit_ns).
+// The bounded waits' limit (tq_set_wait_limit_ns), and whether kernels are to
+// withhold their hand-offs (tq_test_withhold_handoffs).
 unsigned long long wait_limit_ns();
+int handoffs_withheld();
 
 }  // namespace tq

@@ -609,3 +609,97 @@ def test_captured_steps_follow_the_batch():
         torch.cuda.synchronize()
         for t in io:
             assert torch.equal(t[2], want[i])
+
+
+def test_bounded_waits_give_up():
+    """With the copies withheld and the wait limit at 2 ms every call returns: NaN rows and the device's error word (append:
+    the pages stay as they were), and the next calls are right."""
+    st = Setup(128, 2, 64, (100, 300), seed=3)
+    kv = st.fill()
+    q = torch.randn(2, 8, 128, device=DEV).to(BF16)
+    out = torch.zeros_like(q)
+    ws = tq.paged_workspace_for(st.cache, st.batch, 8)
+    x = torch.randn(200, 2, 128, device=DEV).to(BF16)
+    po = torch.zeros_like(x)
+    cu = _cu([50, 150])
+    tq.tq_device_errors(clear=True)
+    try:
+        tq.tq_set_wait_limit_ns(2_000_000)
+        tq.tq_test_withhold_handoffs(True)
+        tq.tq_paged_decode_attention(st.cache, st.batch, q, out, ws)
+        assert tq.tq_device_errors(clear=True) == tq.ERRF_DECODE_WAIT
+        tq.tq_prompt_attention(x, x, x, cu, cu, po)
+        assert tq.tq_device_errors(clear=True) == tq.ERRF_PROMPT_WAIT
+        tq.tq_paged_append(st.cache, st.batch, cu, x, x)
+        assert tq.tq_device_errors(clear=True) == tq.ERRF_QUANTIZE_WAIT
+    finally:
+        tq.tq_test_withhold_handoffs(False)
+        tq.tq_set_wait_limit_ns(0)
+    assert torch.isnan(out).all() and torch.isnan(po).all()
+    assert np.array_equal(st.buffer.cpu().numpy(), st.host)
+    tq.tq_paged_decode_attention(st.cache, st.batch, q, out, ws)
+    _check_decode(st, kv, q, out, 128 ** -0.5)
+    tq.tq_prompt_attention(x, x, x, cu, cu, po)
+    _check_prompt(x, x, x, [50, 150], [50, 150], po, 128 ** -0.5, lambda n: {0, n - 1})
+    assert tq.tq_device_errors() == 0
+
+
+def test_another_stream_and_lengths_out_of_range():
+    """Calls on a side stream (inputs made on it), and lengths and first positions at the ends of 32 bits: nothing is
+    dereferenced, rows are NaN, zero or left as the lengths say."""
+    st = Setup(64, 1, 16, (20, 33), seed=4, fill=0x33)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        x = torch.randn(53, 1, 64, device=DEV)
+        tq.tq_paged_append(st.cache, st.batch, _cu([20, 33]), x, x)
+        k, v = torch.zeros_like(x), torch.zeros_like(x)
+        tq.tq_paged_gather(st.cache, st.batch, _cu([20, 33]), k, v)
+    side.synchronize()
+    rec = paged.encode(_np(x)[:, 0])
+    want = (rec["codes"] * rec["scale16"].repeat(32, 1) + rec["zero16"].repeat(32, 1)).astype(np.float32)
+    assert np.array_equal(k[:, 0].cpu().numpy(), want) and torch.equal(k, v)
+    before = st.buffer.clone()
+    q = torch.randn(2, 4, 64, device=DEV).to(BF16)
+    out = torch.zeros_like(q)
+    ws = tq.paged_workspace_for(st.cache, st.batch, 4)
+    tq.tq_device_errors(clear=True)
+    for lens in ([2 ** 31 - 1, -2 ** 31], [-5, 2 ** 30 + 7]):
+        st.batch.len_dev.copy_(_i32(lens))
+        tq.tq_paged_append(st.cache, st.batch, _cu([20, 33]), x, x)
+        assert torch.equal(st.buffer, before)
+        assert tq.tq_device_errors(clear=True) == tq.ERRF_PAGE
+        tq.tq_paged_decode_attention(st.cache, st.batch, q, out, ws)
+        for b, n in enumerate(lens):
+            assert torch.isnan(out[b]).all() if n > 0 else not out[b].any()
+        tq.tq_device_errors(clear=True)
+    st.batch.len_dev.copy_(_i32([20, 33]))
+    for first in ([2 ** 31 - 1, -2 ** 31], [17, 40]):
+        k.fill_(1.0)
+        tq.tq_paged_gather(st.cache, st.batch, _cu([20, 33]), k, v, first=_i32(first))
+        if first[0] == 17:
+            assert torch.equal(k[:3, 0].cpu(), torch.from_numpy(want[17:20])) and torch.isnan(k[3:]).all()
+        else:
+            assert torch.isnan(k).all()
+    assert tq.tq_device_errors(clear=True) == tq.ERRF_PAGE
+
+
+@pytest.mark.parametrize("start", [0, 40])
+def test_rows_before_the_first_sequence_and_repeated_boundaries(start):
+    """Row arrays whose first entry is not 0: the rows before it belong to nobody and are left as they are."""
+    st = Setup(64, 1, 16, (9, 0, 0, 30), seed=5, fill=0)
+    T = start + 39 + 4
+    cu = _i32([start, start + 9, start + 9, start + 9, start + 39])
+    x = torch.randn(T, 1, 64, device=DEV).to(BF16)
+    ko = torch.full_like(x, 2.0)
+    tq.tq_paged_append(st.cache, st.batch, cu, x, x, k_out=ko)
+    k, v, o = (torch.full_like(x, 2.0) for _ in range(3))
+    tq.tq_paged_gather(st.cache, st.batch, cu, k, v)
+    tq.tq_prompt_attention(x, x, x, cu, cu, o)
+    assert torch.equal(ko[start : start + 39], x[start : start + 39])
+    for y in (ko, k, v, o):
+        assert (y[:start] == 2.0).all() and (y[start + 39 :] == 2.0).all()
+    rec = paged.encode(_np(x)[start : start + 39, 0])
+    want = torch.from_numpy(rec["codes"] * rec["scale16"].repeat(32, 1) + rec["zero16"].repeat(32, 1)).float().to(BF16)
+    assert torch.equal(k[start : start + 39, 0].cpu(), want)
+    y = x[start:]
+    _check_prompt(y, y, y, [9, 0, 0, 30], [9, 0, 0, 30], o[start:], 64 ** -0.5)

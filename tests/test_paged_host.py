@@ -60,7 +60,7 @@ def test_bad_batches(batch, want):
     (dict(dt=3), 2), (dict(T=-1), 1), (dict(T=0, k=None, v=None), 0), (dict(cu=None), 1), (dict(k=None), 1), (dict(v=None), 1),
     (dict(k=A + 8), 1), (dict(ks=1023), 1), (dict(ks=1028), 1), (dict(vs=512), 1), (dict(q=A + 2), 1), (dict(qo=None), 1),
     (dict(hq=12), 1), (dict(hq=4), 1), (dict(qs=4000), 1), (dict(ko=A + 8), 1), (dict(ko=A, kos=2048), 1),
-    (dict(qo=A, qos=8192), 1), (dict(T=0x7fffffff), 3)])
+    (dict(qo=A, qos=8192), 1), (dict(T=0x7fffffff), 3), (dict(hq=72, qs=9216, qos=9216), 2)])
 def test_append_refusals(kw, want):
     assert _append(**kw) == want
 
@@ -81,7 +81,7 @@ def test_gather_refusals(kw, want):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(q=None), 1), (dict(out=None), 1), (dict(dt=0), 2), (dict(dt=3), 2), (dict(hq=12), 1), (dict(hq=4), 1), (dict(hq=72), 2),
-    (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(qs=128), 1), (dict(os=4100), 1), (dict(ws=None), 4),
+    (dict(scale=float("inf")), 1), (dict(scale=float("nan")), 1), (dict(scale=3e38), 1), (dict(qs=128), 1), (dict(os=4100), 1), (dict(ws=None), 4),
     (dict(ws=A + 16), 4)])
 def test_decode_refusals(kw, want):
     x = dict(q=A, dt=1, hq=32, qs=4096, scale=0.1, out=A, os=4096, ws=A, wsb=1 << 30) | kw
@@ -94,7 +94,7 @@ def test_decode_refusals(kw, want):
 @pytest.mark.parametrize("kw,want", [
     (dict(q=None), 1), (dict(k=None), 1), (dict(out=None), 1), (dict(dt=0), 2), (dict(d=80), 2), (dict(hq=12), 1), (dict(hkv=0), 1),
     (dict(hq=72), 2), (dict(Tq=-1), 1), (dict(Tk=-1), 1), (dict(batch=0), 1), (dict(cu=None), 1), (dict(cu=A + 2), 1),
-    (dict(scale=float("nan")), 1), (dict(qs=64), 1), (dict(vs=1028), 1), (dict(Tq=0, q=None), 0), (dict(Tq=(1 << 30) + 1), 3),
+    (dict(scale=float("nan")), 1), (dict(scale=-3e38), 1), (dict(qs=64), 1), (dict(vs=1028), 1), (dict(Tq=0, q=None), 0), (dict(Tq=(1 << 30) + 1), 3),
     (dict(batch=(1 << 20) + 1), 3)])
 def test_prompt_refusals(kw, want):
     x = dict(q=A, k=A, v=A, dt=1, Tq=4, Tk=4, hq=32, hkv=8, d=128, qs=1 << 14, ks=1024, vs=1024, cu=A, batch=2, scale=0.1, out=A,
