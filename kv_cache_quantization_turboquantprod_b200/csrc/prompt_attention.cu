@@ -395,9 +395,9 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       tc_fence_after();
       const uint32_t st = tmem + C::s_col(buf) + lanes + part * KH;
       const int vis = (j + 1) * KT > easy ? lim - j * KT - part * KH : KH;  // keys of the half that the row sees
-      // 32 scores, masked ones -inf.  (They are read twice, for the maximum and
-      // for the weights: tensor memory is nearer than the registers that all of
-      // them would take.)
+      // 32 scores, masked ones -inf.  (The first 32 stay in registers between the
+      // maximum and the weights; the others are read twice: tensor memory is
+      // nearer than the registers that all of them would take.)
       auto load = [&](int i, uint32_t (&s)[32]) {
         tmem_ld32(st + 32 * i, s);
         tmem_wait_ld();
@@ -408,10 +408,10 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
         }
       };
       float top = -INFINITY;
+      uint32_t s[32];
       if (ok) {
 #pragma unroll
-        for (int i = 0; i < KH / 32; ++i) {
-          uint32_t s[32];
+        for (int i = KH / 32 - 1; i >= 0; --i) {
           load(i, s);
           float top2 = -INFINITY;
 #pragma unroll
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < KH / 32; ++i) {
-        uint32_t s[32], p[16];
-        load(i, s);
+        uint32_t p[16];
+        if (i > 0) load(i, s);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, mc2);
