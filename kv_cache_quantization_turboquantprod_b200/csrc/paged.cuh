@@ -100,6 +100,35 @@ __device__ __forceinline__ int unit_sequence(const int32_t *cu, int batch, int r
   return lo;
 }
 
+// A unit's sequence, its rows and two of its entries (x, y: [batch], y may be
+// null).  Up to 32 sequences: every lane loads one's, so that one memory
+// latency passes instead of three.
+struct Unit {
+  int b, r0, r1, x, y;
+};
+template <int S>
+__device__ __forceinline__ Unit find_unit(const int32_t *cu, const int32_t *x, const int32_t *y, int batch, int rows, int u) {
+  Unit t;
+  if (batch <= 32) {
+    const int lane = threadIdx.x & 31, i = min(lane, batch - 1);
+    const int c0 = clamp_cu(cu, i, rows), c1 = clamp_cu(cu, i + 1, rows), xi = x[i], yi = y ? y[i] : 0;
+    const bool below = lane < batch && (c0 >> S) + 2 * lane <= u;
+    t.b = max(__popc(__ballot_sync(0xffffffffu, below)) - 1, 0);
+    t.r0 = __shfl_sync(0xffffffffu, c0, t.b);
+    t.r1 = __shfl_sync(0xffffffffu, c1, t.b);
+    t.x = __shfl_sync(0xffffffffu, xi, t.b);
+    t.y = __shfl_sync(0xffffffffu, yi, t.b);
+  } else {
+    t.b = unit_sequence<S>(cu, batch, rows, u);
+    t.r0 = clamp_cu(cu, t.b, rows);
+    t.r1 = clamp_cu(cu, t.b + 1, rows);
+    t.x = x[t.b];
+    t.y = y ? y[t.b] : 0;
+  }
+  t.r1 = max(t.r1, t.r0);
+  return t;
+}
+
 // Rows as 32-bit values: eight consecutive elements of T.
 template <class T>
 __device__ __forceinline__ void load8(const T *p, float (&x)[8]) {

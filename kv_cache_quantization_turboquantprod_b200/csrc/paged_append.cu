@@ -162,9 +162,9 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) paged_append_kernel(con
     sm100::fence_mbar_init();
   }
   const int h = blockIdx.x % a.c.h_kv, u = blockIdx.x / a.c.h_kv;
-  const int b = unit_sequence<4>(a.cu, a.c.batch, a.T, u);
-  const int r0 = clamp_cu(a.cu, b, a.T), r1 = max(clamp_cu(a.cu, b + 1, a.T), r0);
-  const int first = clamp_position(a.c.len[b]) - (r1 - r0);  // position of row r0
+  const Unit unit = find_unit<4>(a.cu, a.c.len, nullptr, a.c.batch, a.T, u);
+  const int b = unit.b, r0 = unit.r0, r1 = unit.r1;
+  const int first = clamp_position(unit.x) - (r1 - r0);  // position of row r0
   const int cell = (first >> 4) + u - ((r0 >> 4) + 2 * b);
   // rows of this cell: positions 16 cell .. 16 cell + 15
   const int lo = max(16 * cell, first), hi = min(16 * cell + 16, first + (r1 - r0));

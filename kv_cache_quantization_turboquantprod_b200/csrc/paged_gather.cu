@@ -26,13 +26,11 @@ __global__ void __launch_bounds__(32 * kWarps) paged_gather_kernel(const __grid_
   const int h = (int)(id % a.c.h_kv);
   const long long u = id / a.c.h_kv;
   if (u >= span_units<4>(a.rows, a.c.batch)) return;
-  const int b = unit_sequence<4>(a.cu, a.c.batch, a.rows, (int)u);
-  const int r0 = clamp_cu(a.cu, b, a.rows), r1 = max(clamp_cu(a.cu, b + 1, a.rows), r0);
-  const int first = a.first ? clamp_position(a.first[b]) : 0;
+  const Unit unit = find_unit<4>(a.cu, a.c.len, a.first, a.c.batch, a.rows, (int)u);
+  const int b = unit.b, r0 = unit.r0, r1 = unit.r1, first = clamp_position(unit.y), len = unit.x;
   const int cell = (first >> 4) + (int)u - ((r0 >> 4) + 2 * b);
   const int lo = max(16 * cell, first), hi = min(16 * cell + 16, first + (r1 - r0));
   if (lo >= hi) return;
-  const int len = a.c.len[b];
   const int page = page_of(a.c, b, lo);
   if (lane == 0 && (page < 0 || hi > len)) atomicOr(a.c.errors, TQ_ERRF_PAGE);
   uint8_t *const img = cells[warp];
