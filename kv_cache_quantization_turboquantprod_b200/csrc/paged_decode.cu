@@ -77,8 +77,8 @@ struct Smem {
   static constexpr int kBars = kRing;                            // [kWarps][kStages] u64
   static constexpr int kScan = kBars + kWarps * kStages * 8;     // 16 long long
   static constexpr int kInfo = kScan + 128;                      // [kWarps][2] Record
-  static constexpr int kState = kInfo + kWarps * 2 * 16;         // [kWarps][8][2] floats: M, l of the first records
-  static constexpr int kMerge = kState + kWarps * 8 * 2 * 4;     // [kWarps][G][D] floats: their sums
+  static constexpr int kState = kInfo + kWarps * 2 * 16;         // [kWarps][2][8][2] floats: the records' M and l
+  static constexpr int kMerge = kState + kWarps * 2 * 8 * 2 * 4; // [kWarps][G][D] floats: sums of the first ones
   static constexpr size_t bytes(int G) { return kMerge + (size_t)kWarps * G * D * 4; }
 };
 
@@ -631,9 +631,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     if (bad || dead) ps[0] = ps[1] = __int_as_float(0x7fffffff);
     const int ends = (here.step == 0 ? 1 : 0) | (here.step + end - at == here.steps ? 2 : 0);
     const int slot = 2 * warp + (at == begin ? 0 : 1);
-    // the last record lies in the warp's own ring, whose copies have all been used
+    // the last record's sums lie in the warp's own ring, whose copies have all been used
+    // (or its l is NaN: a copy that a warp gave up waiting for may still land there)
     float *const rec = at == begin ? merge + (size_t)warp * G * D : reinterpret_cast<float *>(ring);
-    float *const rec_state = at == begin ? state + warp * 16 : rec + G * D;
+    float *const rec_state = state + slot * 16;
     if (ends != 3) {
       __syncwarp();
       if (g == 0)
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       auto sums = [&](int k) {
         return k & 1 ? reinterpret_cast<const float *>(smem + (k / 2) * kStages * S::kStage) : merge + (size_t)(k / 2) * G * D;
       };
-      auto states = [&](int k) { return (k & 1 ? sums(k) + G * D : state + (k / 2) * 16) + 2 * h; };
+      auto states = [&](int k) { return state + k * 16 + 2 * h; };
       for (int k = r; k <= last; ++k)
         if (info[k].place >= 0) top = fmaxf(top, states(k)[0]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
