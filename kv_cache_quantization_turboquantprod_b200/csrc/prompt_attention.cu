@@ -58,7 +58,8 @@ using namespace sm100;
 template <int D, int NQ>
 struct Prompt {
   static_assert(D < 256 || NQ == 1, "two tiles' O do not fit beside S");
-  static constexpr bool kTwoBufs = NQ == 1;         // S buffers of a tile
+  static constexpr int kBufs = NQ == 2 && D == 64 ? 3 : 2;  // S buffers
+  static constexpr bool kAhead = kBufs > NQ;        // a tile's scores may come before its last weights are used
   static constexpr int kBlocks = NQ == 2 || D == 256 ? 1 : 2;  // blocks of an SM
   static constexpr int kKeys = NQ == 2 ? 128 : 64;  // keys of a step
   static constexpr bool kHalves = kKeys == 128;     // P is handed over in two halves
@@ -74,7 +75,7 @@ struct Prompt {
   // tensor memory columns: S (and P over it) of buffer or tile x, O of tile x
   static constexpr uint32_t kColumns = kBlocks == 2 ? 256 : 512;
   __host__ __device__ static constexpr uint32_t s_col(int x) { return (uint32_t)kKeys * x; }
-  __host__ __device__ static constexpr uint32_t o_col(int x) { return 2u * kKeys + (uint32_t)D * x; }
+  __host__ __device__ static constexpr uint32_t o_col(int x) { return (uint32_t)(kBufs * kKeys) + (uint32_t)D * x; }
   // P of keys 16 k .. + 15, from the S buffer's first column: each half over the first half of its own S
   __host__ __device__ static constexpr uint32_t p_col(int k) {
     return k < kKeys / 32 ? 8u * k : (uint32_t)kKeys / 2 + 8u * (k - kKeys / 32);
@@ -126,16 +127,17 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int units) {
   using C = Prompt<D, NQ>;
   constexpr int KT = C::kKeys, ST = C::kStages;
-  constexpr bool kBf16 = __is_same(T, __nv_bfloat16), kTwoBufs = C::kTwoBufs;
+  constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
+  constexpr int NB = C::kBufs;
   extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms)
   uint8_t *const stages = smem + NQ * C::kQTile;
   float *const exchange = reinterpret_cast<float *>(smem + C::kExchange);
   int *const exchange_ok = reinterpret_cast<int *>(exchange + NQ * 256), *const bad = reinterpret_cast<int *>(smem + C::kBad);
   uint64_t *const bars = reinterpret_cast<uint64_t *>(smem + C::kBars);
-  // [2]: by buffer (NQ = 1) or by tile
+  // s_full, p_ready and p_half: by S buffer; o_done: by tile
   uint64_t *const q_full = bars, *const kv_full = bars + 1, *const kv_empty = kv_full + ST, *const s_full = kv_empty + ST,
-                  *const p_ready = s_full + 2, *const p_half = p_ready + 2, *const o_done = p_half + 2,
-                  *const v_here = o_done + 1, *const v_clear = v_here + ST, *const drained = v_clear + ST;
+                  *const p_ready = s_full + NB, *const p_half = p_ready + NB, *const o_done = p_half + NB,
+                  *const v_here = o_done + 2, *const v_clear = v_here + ST, *const drained = v_clear + ST;
   uint32_t *const tmem_slot = reinterpret_cast<uint32_t *>(drained + 1);
   volatile int *const abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   // the block's first row, its tokens and first head, for the end (out of the registers until then); [3]: V had
@@ -169,12 +171,12 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       mbar_init(&v_here[s], 1);
       mbar_init(&v_clear[s], 2);
     }
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < NB; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_ready[x], 8);
       mbar_init(&p_half[x], 8);
     }
-    mbar_init(o_done, 1);
+    for (int x = 0; x < NQ; ++x) mbar_init(&o_done[x], 1);
     mbar_init(drained, 1);
     *abort_flag = 0;
     place[0] = q0 + i0;
@@ -197,6 +199,13 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
   // for a whole warp: its lanes go on, or give up, together
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     return (bool)__all_sync(0xffffffffu, pipe_wait(bar, parity, abort_flag, a.wait_ns, hint, &timed_out));
+  };
+
+  // Scores and weights of (step, tile) in turn go through the S buffers: the
+  // place of tile x's step j in that order.  (Where the second tile has steps, the first has no more.)
+  const int steps0 = steps_of(0), steps1 = NQ == 2 ? steps_of(1) : 0;
+  auto turn_of = [&](int x, int j) {
+    return NQ == 1 || steps1 == 0 ? j : x == 0 ? 2 * j : j < steps0 ? 2 * j + 1 : steps0 + j;
   };
 
   // which use of its stage among the steps that are looked at V of step j is: V's place comes round every so many steps
@@ -263,7 +272,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
             if (leader)
               mma_f16_ts(tmem + C::o_col(x), tmem + C::s_col(buf) + C::p_col(k), vt + (uint32_t)(k * 128), io, j > 0 || k > 0);
           }
-        if (kTwoBufs && leader) mma_commit(o_done);
+        if (C::kAhead && which != 0 && leader) mma_commit(&o_done[x]);
       };
       auto release = [&](Place &p) {
         if (leader) mma_commit(&kv_empty[p.st]);
@@ -275,58 +284,55 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
         if (!landed(vp)) return false;
         return j < looked || wait(&v_clear[vp.st], use_of(j));
       };
-      bool ok = most == 0 || (wait(q_full, 0) && landed(kp));
-      tc_fence_after();
-      if (ok && most > 0) {
-#pragma unroll
-        for (int x = 0; x < NQ; ++x)
-          if (steps_of(x) > 0) scores(x, x);
-        release(kp);
-      }
-      if constexpr (kTwoBufs) {
-        for (int j = 0; ok && j < most; ++j) {
-          if (j + 1 < most) {
-            ok = landed(kp);
-            tc_fence_after();
-            if (!ok) break;
-            scores(0, (j + 1) & 1);
-            release(kp);
-          }
-          ok = value_tile(j) && wait(&p_ready[j & 1], (j >> 1) & 1);
+      // the (step, tile) whose scores, and whose products with V, come next
+      struct Turn {
+        int x, j, buf;
+        uint32_t phase;
+      } sc{steps0 > 0 ? 0 : NQ - 1, 0, 0, 0}, pv = sc;
+      auto starts = [&](const Turn &t) { return t.x == 0 || t.j >= steps0; };      // its step's first tile, last tile
+      auto ends = [&](const Turn &t) { return t.x == NQ - 1 || t.j >= steps1; };
+      auto advance = [&](Turn &t) {
+        if (ends(t)) {
+          ++t.j;
+          t.x = t.j < steps0 ? 0 : NQ - 1;
+        } else {
+          t.x = 1;
+        }
+        if (++t.buf == NB) {
+          t.buf = 0;
+          t.phase ^= 1;
+        }
+      };
+      // (each K and V tile is asked for just before its first use and given back
+      // just after its last, or the copies do not come in time)
+      auto next_scores = [&] {
+        if (sc.j >= most) return true;
+        // not before the tile's products of two steps earlier: whoever has these scores knows those done, and can
+        // tell the step between by o_done's parity
+        if (NB > 2 && (pv.j < sc.j - 2 || (pv.j == sc.j - 2 && pv.x <= sc.x))) return true;
+        if (starts(sc) && !landed(kp)) return false;
+        tc_fence_after();
+        scores(sc.x, sc.buf);
+        if (ends(sc)) release(kp);
+        advance(sc);
+        return true;
+      };
+      bool ok = most == 0 || wait(q_full, 0);
+      for (int i = 0; ok && i < NB; ++i) ok = next_scores();
+      while (ok && pv.j < most) {
+        if (starts(pv)) ok = value_tile(pv.j);
+        if (ok && C::kHalves) {
+          ok = wait(&p_half[pv.buf], pv.phase);
           tc_fence_after();
-          if (!ok) break;
-          values(0, j & 1, j, 2);
-          release(vp);
+          if (ok) values(pv.x, pv.buf, pv.j, 0);
         }
-      } else {
-        const int steps[2] = {steps_of(0), steps_of(1)};
-        for (int j = 0; ok && j < most; ++j) {
-          // (each tile is asked for just before its first use and given back just
-          // after its last, or the copies do not come in time)
-          ok = value_tile(j);
-          bool next = false;  // K(j + 1) is here
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (ok && j < steps[x]) {
-              ok = wait(&p_half[x], j & 1);
-              tc_fence_after();
-              if (ok) {
-                values(x, x, j, 0);
-                ok = wait(&p_ready[x], j & 1);
-                tc_fence_after();
-              }
-              if (ok) values(x, x, j, 1);
-            }
-            if (ok && x == 1) release(vp);
-            if (ok && j + 1 < steps[x]) {
-              if (!next) ok = landed(kp);
-              next = true;
-              tc_fence_after();
-              if (ok) scores(x, x);
-            }
-          }
-          if (ok && j + 1 < most) release(kp);
-        }
+        ok = ok && wait(&p_ready[pv.buf], pv.phase);
+        tc_fence_after();
+        if (!ok) break;
+        values(pv.x, pv.buf, pv.j, C::kHalves ? 1 : 2);
+        if (ends(pv)) release(vp);
+        advance(pv);
+        ok = next_scores();
       }
       // tensor and shared memory stay until every product has finished
       if (leader) mma_commit(drained);
@@ -385,13 +391,13 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
     const uint32_t lanes = (uint32_t)quarter * 32u << 16;
     // keys that this row sees, and that every row of the tile sees (rows that
     // belong to no token go on as if they did; nothing reads them)
-    const int lim = min(nk, i0 + x * tpt + r / G + 1 + shift), easy = min(nk, i0 + x * tpt + 1 + shift), steps = steps_of(x);
+    const int lim = min(nk, i0 + x * tpt + r / G + 1 + shift), easy = min(nk, i0 + x * tpt + 1 + shift), steps = x ? steps1 : steps0;
     const float c = a.scale_log2;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < steps; ++j) {
-      const int buf = kTwoBufs ? j & 1 : x;
-      ok = wait(&s_full[buf], kTwoBufs ? (j >> 1) & 1 : j & 1);
+      const int turn = turn_of(x, j), buf = turn % NB;
+      ok = wait(&s_full[buf], turn / NB & 1);
       tc_fence_after();
       const uint32_t st = tmem + C::s_col(buf) + lanes + part * KH;
       const int vis = (j + 1) * KT > easy ? lim - j * KT - part * KH : KH;  // keys of the half that the row sees
@@ -436,8 +442,8 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
         const float f = was == m ? 1.f : ex2_approx((was - m) * c);  // was = -inf: 0
         l *= f;
         if (j > 0) {
-          if constexpr (kTwoBufs) {  // (with one buffer the scores were issued behind it)
-            ok = wait(o_done, (j - 1) & 1);
+          if constexpr (C::kAhead) {  // (or the scores were issued behind it)
+            ok = wait(&o_done[x], (j - 1) & 1);
             tc_fence_after();
           }
           const uint32_t ot = tmem + C::o_col(x) + lanes + part * DH;
