@@ -62,7 +62,7 @@ struct Prompt {
   static constexpr bool kAhead = kBufs > NQ;        // a tile's scores may come before its last weights are used
   static constexpr int kBlocks = NQ == 2 || D == 256 ? 1 : 2;  // blocks of an SM
   static constexpr int kKeys = NQ == 2 ? 128 : 64;  // keys of a step
-  static constexpr bool kHalves = kKeys == 128;     // P is handed over in two halves
+  static constexpr bool kHalves = kKeys == 128 && !kAhead;  // P is handed over in two halves
   static constexpr int kSlabs = D / 64;             // 64-channel boxes
   static constexpr int kQSlab = 128 * 128, kSlab = kKeys * 128;
   static constexpr int kQTile = kQSlab * kSlabs, kStage = kSlab * kSlabs;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
     } else if (warp == 1) {
       // ---- products.  The whole warp runs the loop, so that descriptors stay in
       // uniform registers; one lane issues.
-      const bool leader = elect_one();
+      const uint32_t leader = elect_one();
       const uint32_t is = idesc_16bit(128, KT, kBf16, false, a.negate), io = idesc_16bit(128, D, kBf16, true, false);
       const uint32_t sa = smem_u32(stages);
       const uint64_t qd = smem_desc_sw128(smem_u32(smem), 16, 1024), kd = smem_desc_sw128(sa, 16, 1024),
@@ -258,24 +258,22 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
         const uint64_t kt = kd + (uint32_t)(kp.st * (C::kStage >> 4));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          if (leader)
-            mma_f16_ss(tmem + C::s_col(buf), qd + (uint32_t)((x * C::kQTile + (k / 4) * C::kQSlab + (k % 4) * 32) >> 4),
-                       kt + (uint32_t)(((k / 4) * C::kSlab + (k % 4) * 32) >> 4), is, k > 0);
-        if (leader) mma_commit(&s_full[buf]);
+          mma_f16_ss_if(leader, tmem + C::s_col(buf), qd + (uint32_t)((x * C::kQTile + (k / 4) * C::kQSlab + (k % 4) * 32) >> 4),
+                        kt + (uint32_t)(((k / 4) * C::kSlab + (k % 4) * 32) >> 4), is, k > 0);
+        mma_commit_if(leader, &s_full[buf]);
       };
       // O[x] += P V over the first 32 keys of each half, over the others, or over all
       auto values = [&](int x, int buf, int j, int which) {
         const uint64_t vt = vd + (uint32_t)(vp.st * (C::kStage >> 4));
 #pragma unroll
         for (int k = 0; k < KT / 16; ++k)
-          if (which == 2 || (k >> 1 & 1) == which) {
-            if (leader)
-              mma_f16_ts(tmem + C::o_col(x), tmem + C::s_col(buf) + C::p_col(k), vt + (uint32_t)(k * 128), io, j > 0 || k > 0);
-          }
-        if (C::kAhead && which != 0 && leader) mma_commit(&o_done[x]);
+          if (which == 2 || (k >> 1 & 1) == which)
+            mma_f16_ts_if(leader, tmem + C::o_col(x), tmem + C::s_col(buf) + C::p_col(k), vt + (uint32_t)(k * 128), io,
+                          j > 0 || k > 0);
+        if (C::kAhead && which != 0) mma_commit_if(leader, &o_done[x]);
       };
       auto release = [&](Place &p) {
-        if (leader) mma_commit(&kv_empty[p.st]);
+        mma_commit_if(leader, &kv_empty[p.st]);
         p.advance();
       };
       auto landed = [&](const Place &p) { return wait(&kv_full[p.st], p.phase); };
@@ -335,7 +333,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
         ok = next_scores();
       }
       // tensor and shared memory stay until every product has finished
-      if (leader) mma_commit(drained);
+      mma_commit_if(leader, drained);
       __syncwarp();
       mbar_wait(drained, 0);
     } else {
