@@ -318,6 +318,37 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       bool ok = most == 0 || wait(q_full, 0);
       for (int i = 0; ok && i < NB; ++i) ok = next_scores();
       while (ok && pv.j < most) {
+        if (NQ == 2 && pv.x == 0 && pv.j + 2 < steps0 && sc.x == NB - 2 && sc.j == pv.j + 1) {
+          // a whole step in the middle, the same turns without their case distinctions: after the products of a
+          // buffer's weights, that buffer's next scores
+#pragma unroll
+          for (int x = 0; x < NQ; ++x) {
+            if (x == 0) ok = value_tile(pv.j);
+            if (ok && C::kHalves) {
+              ok = wait(&p_half[pv.buf], pv.phase);
+              tc_fence_after();
+              if (ok) values(x, pv.buf, pv.j, 0);
+            }
+            ok = ok && wait(&p_ready[pv.buf], pv.phase);
+            tc_fence_after();
+            if (!ok) break;
+            values(x, pv.buf, pv.j, C::kHalves ? 1 : 2);
+            if (x == 1) release(vp);
+            const int y = NB == 3 ? 1 - x : x;  // the scores' tile
+            if (y == 0) ok = landed(kp);
+            tc_fence_after();
+            if (!ok) break;
+            scores(y, pv.buf);
+            if (y == 1) release(kp);
+            const bool wraps = pv.buf == NB - 1;
+            pv.buf = wraps ? 0 : pv.buf + 1;
+            pv.phase ^= wraps;
+          }
+          sc.buf = pv.buf;
+          ++pv.j;
+          ++sc.j;
+          continue;
+        }
         if (starts(pv)) ok = value_tile(pv.j);
         if (ok && C::kHalves) {
           ok = wait(&p_half[pv.buf], pv.phase);
