@@ -21,7 +21,7 @@
 // the end.  One tile's softmax runs under the other's products, or one step's
 // under the next one's (two S buffers); P is handed over in halves where a
 // step has 128 keys, so that products start under the second half's
-// exponentials; a quarter of these are polynomials.
+// exponentials; an eighth of these are polynomials.
 //
 // The running maximum only moves when a row's grows by more than 2^8 (P stays
 // in range of both types, and the sum in float32), so a row's two threads
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, mc2);
-          if (D < 256 && e % 4 == 3) {  // a quarter of them, so that neither unit waits for the other
+          if (e % 8 == 7) {  // an eighth of them: the exponential unit's queue is the shorter for it
             y = exp2_poly(y);
           } else {
             y.x = ex2_approx(y.x);
@@ -651,10 +651,12 @@ cudaError_t launch_d(const PromptArgs &a, cudaStream_t stream) {
   // Long sequences: two tiles share the keys' copies and operand reads, and
   // products of 128 keys read shared memory at the rate the tensor pipe takes.
   // Short ones: two blocks an SM hide each other's start and end.  32/8 heads,
-  // d = 128, bf16: 8192 tokens 446 us (one tile a block: 499), 4 x 2048 158 (158),
-  // 32 x 512 165 (143), 16 ragged up to 2000 272 (256); d = 64, 8192 tokens 378 (394).
+  // us with two tiles a block (one tile): d = 128, bf16: 2 x 4096 tokens 246
+  // (262), 1 x 2048 41 (43), 4 x 2048 154 (153), 8 x 1536 196 (187), 32 x 512
+  // 167 (145); d = 64, fp16, where two tiles have a third score buffer: 2 x
+  // 4096 194 (222), 8 x 1536 159 (164), 16 x 1024 172 (169), 32 x 512 139 (124).
   if constexpr (D < 256) {
-    if (a.T_k > 2048ll * a.batch) return launch<D, T, 2>(a, stream);
+    if (a.T_k >= (D == 64 ? 1280ll : 2048ll) * a.batch) return launch<D, T, 2>(a, stream);
   }
   return launch<D, T, 1>(a, stream);
 }
