@@ -305,9 +305,11 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       // just after its last, or the copies do not come in time)
       auto next_scores = [&] {
         if (sc.j >= most) return true;
-        // not before the tile's products of two steps earlier: whoever has these scores knows those done, and can
-        // tell the step between by o_done's parity
-        if (NB > 2 && (pv.j < sc.j - 2 || (pv.j == sc.j - 2 && pv.x <= sc.x))) return true;
+        // Where a tile goes on alone the buffers would let its scores come further ahead.  Not before the tile's
+        // products of a step earlier (two, with buffers to come ahead): whoever has these scores knows those done
+        // (and can tell the step between by o_done's parity), and may change O.
+        constexpr int kBack = C::kAhead ? 2 : 1;
+        if (NQ == 2 && (pv.j < sc.j - kBack || (pv.j == sc.j - kBack && pv.x <= sc.x))) return true;
         if (starts(sc) && !landed(kp)) return false;
         tc_fence_after();
         scores(sc.x, sc.buf);
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlock
       bool ok = most == 0 || wait(q_full, 0);
       for (int i = 0; ok && i < NB; ++i) ok = next_scores();
       while (ok && pv.j < most) {
-        if (NQ == 2 && pv.x == 0 && pv.j + 2 < steps0 && sc.x == NB - 2 && sc.j == pv.j + 1) {
+        if (NQ == 2 && pv.x == 0 && pv.j + 2 < min(steps0, steps1) && sc.x == NB - 2 && sc.j == pv.j + 1) {
           // a whole step in the middle, the same turns without their case distinctions: after the products of a
           // buffer's weights, that buffer's next scores
 #pragma unroll

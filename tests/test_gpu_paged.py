@@ -475,6 +475,46 @@ def test_prompt_special_values_reach_only_who_sees_them(d, h_q, h_kv, dtype, lon
     assert torch.equal(out[want], clean[want])
 
 
+def _check_on_device(q, k, v, new, nk, out):
+    h_q, h_kv, d, dt = q.shape[1], k.shape[1], q.shape[2], q.dtype
+    a = c = 0
+    for n, m in zip(new, nk):
+        i, j = torch.arange(n, device=DEV)[:, None], torch.arange(m, device=DEV)
+        seen = (i[:, 0] + m - n >= 0).cpu().numpy()
+        for hq in range(h_q):
+            kk, vv = (x[c : c + m, hq * h_kv // h_q].double() for x in (k, v))
+            s = q[a : a + n, hq].double() @ kk.T * d ** -0.5
+            w = torch.softmax(s.masked_fill(j > i + m - n, -torch.inf), -1)
+            big = float((q[a : a + n, hq].double().abs() @ kk.abs().T).max() * d ** -0.5)
+            o, got = _np(w @ vv), _np(out[a : a + n, hq])
+            tol = _tolerance(o, _np(w @ vv.abs()), big, d, dt, dt)
+            assert (np.abs(got - o) <= tol)[seen].all(), (n, m, hq)
+            assert not got[~seen].any()
+        a, c = a + n, c + m
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("h_q,h_kv", [(2, 2), (8, 1)])
+@pytest.mark.parametrize("new,nk", [((1,), (2048,)), ((20,), (2100,)), ((300, 100), (170, 4000)), ((100, 700), (2177, 2305)),
+                                    ((129, 257, 31), (2049, 2300, 2048))])
+def test_prompt_two_tiles_of_unlike_lengths(d, h_q, h_kv, new, nk):
+    """Blocks of two tiles whose second has no rows, whose first sees no key, and that see different numbers of steps; keys
+    that grow along the sequence, so that the running maximum moves again and again."""
+    g = torch.Generator(device=DEV).manual_seed(d + h_q)
+    for dt in (BF16, F16):
+        q = torch.randn(sum(new), h_q, d, generator=g, device=DEV).to(dt)
+        grow = torch.cat([torch.linspace(0.25, 8.0, m, device=DEV) for m in nk])[:, None, None]
+        k = (torch.randn(sum(nk), h_kv, d, generator=g, device=DEV) * grow).to(dt)
+        v = torch.randn(sum(nk), h_kv, d, generator=g, device=DEV).to(dt)
+        out = torch.full_like(q, 3.0)
+        tq.tq_prompt_attention(q, k, v, _cu(new), _cu(nk), out)
+        _check_on_device(q, k, v, new, nk, out)
+        again = torch.zeros_like(q)
+        tq.tq_prompt_attention(q, k, v, _cu(new), _cu(nk), again)
+        assert torch.equal(out, again)
+    assert tq.tq_device_errors() == 0
+
+
 def test_prompt_long_against_float64_on_device():
     d, h_q, h_kv, new, past = 128, 8, 2, (2000, 3, 1111), (0, 3000, 517)
     nk = [a + b for a, b in zip(new, past)]
