@@ -82,7 +82,7 @@ struct Prompt {
   }
   // registers of a thread: copies and products, softmax; together at most what
   // the launch has (96, 80 or 168 a thread)
-  static constexpr int kFew = NQ == 2 ? 40 : D == 256 ? 64 : 48, kMany = NQ == 2 ? 104 : D == 256 ? 216 : 96;
+  static constexpr int kFew = 40, kMany = NQ == 2 ? 104 : D == 256 ? 216 : 96;
 };
 
 // 2^y for two y in [-inf, 9] (or NaN) without the exponential unit: y is cut
