@@ -5,7 +5,12 @@
 // score tile is 1024 cycles of products at d = 128), beside it the SM's 16
 // exponentials a cycle (1024 cycles a tile) and shared memory's 128 bytes a
 // cycle (a product of 128 rows x 128 keys reads its operands in the 64 cycles
-// that it takes, one of 64 keys in 48 for 32).
+// that it takes, one of 64 keys in 48 for 32).  Measured, bf16: d = 128, 32/8
+// heads, 8192 tokens 433 us, 1270 TFLOP/s (78% of the rate of one large bf16
+// product; 510 us, the same share, under the power cap); d = 256, 16/8 heads,
+// 467 us, 1177 TFLOP/s; d = 64, 32/8 heads, where exponentials and hand-offs
+// bind, 327 us, 840 TFLOP/s.  Short: 512 tokens, 12/2 heads, 11.2 us, most of
+// it the launch, the first copies and the end.
 //
 // Rows.  A tile's 128 rows are (token, query head of the group) pairs of one
 // KV head: 128 / G tokens with their G heads, so K and V are read once for
@@ -18,10 +23,14 @@
 // tensor memory and V as it lies (MN-major).  Eight softmax warps a tile, two
 // threads a row (one per half of the step's keys), read S, keep the running
 // maximum and sum in float32, write P over S in the operand type and divide at
-// the end.  One tile's softmax runs under the other's products, or one step's
-// under the next one's (two S buffers); P is handed over in halves where a
-// step has 128 keys, so that products start under the second half's
-// exponentials; an eighth of these are polynomials.
+// the end.  Scores and weights of (step, tile) in turn go through two or three
+// S buffers, so that one tile's softmax runs under the other's products, or one
+// step's under the next one's.  Where a tile of 128-key steps has no buffer to
+// come ahead in, P is handed over in halves, so that products start under the
+// second half's exponentials (at d = 64 a third buffer and whole hand-overs
+// take 348 us, halves 355, halves without the third buffer 374).  An eighth of
+// the exponentials are polynomials (8192 tokens at d = 64: none 345 us, a
+// sixteenth 333, an eighth 327, a quarter 342).
 //
 // The running maximum only moves when a row's grows by more than 2^8 (P stays
 // in range of both types, and the sum in float32), so a row's two threads
@@ -53,8 +62,8 @@ namespace {
 using namespace sm100;
 
 // A block's shape.  NQ = 2: two tiles share the keys, 128 a step, one S buffer
-// each, one block an SM.  NQ = 1: one tile, 64 keys a step, two S buffers, two
-// blocks an SM (one at d = 256).
+// each (three for both at d = 64), one block an SM.  NQ = 1: one tile, 64 keys a
+// step, two S buffers, two blocks an SM (one at d = 256).
 template <int D, int NQ>
 struct Prompt {
   static_assert(D < 256 || NQ == 1, "two tiles' O do not fit beside S");
