@@ -7,7 +7,7 @@
 // Measured, d = 128, 32/8 heads, bf16: 16 sequences of 16-32K tokens 102 us,
 // 5.25 TB/s (80% of the copy rate); 32 of them 210 us, 4 x 131072 tokens 142 us
 // (4.8 and 4.7 TB/s, under the power cap); fp16 (two parts of p) 142 us for the
-// 16.  Short work is latency: 1 x 4096 tokens 11.5 us, 61 sequences of up to
+// 16.  Short work is latency: 1 x 4096 tokens 11.6 us, 61 sequences of up to
 // 1500 tokens at d = 256 23 us in bf16, 26 in fp16.
 //
 // Split.  All steps (pairs of cells) of the batch, in the order (sequence, KV
@@ -19,7 +19,7 @@
 // which the block joins once at its end.  A unit that spans blocks goes to the
 // workspace in at most two records a block, which paged_combine_kernel joins
 // in order.  (Joined by the last block to write one, with a counter a unit, it
-// spilled and took 112 us for the 102, 14.2 for the 11.7, and the workspace
+// spilled and took 112 us for the 102, 14.2 for the 11.6, and the workspace
 // had to start as zeros.)
 //
 // A warp is its own pipeline: one lane keeps the next step's bulk copy in
@@ -85,9 +85,16 @@ struct Smem {
   static constexpr int kBars = kRing;                            // [kWarps][kStages] u64
   static constexpr int kScan = kBars + kWarps * kStages * 8;     // 16 long long
   static constexpr int kInfo = kScan + 128;                      // [kWarps][2] Record
-  static constexpr int kState = kInfo + kWarps * 2 * 16;         // [kWarps][2][8][2] floats: the records' M and l
-  static constexpr int kMerge = kState + kWarps * 2 * 8 * 2 * 4; // [kWarps][G][D] floats: sums of the first ones
+  // The last records' M and l lie beside the first ones' where the join reads
+  // them faster (61 sequences at d = 256 22.3 us for 22.8), and behind their
+  // sums at d = 128, where the room would cost an SM its second block (8 query
+  // heads a KV head: 132 us for 104).
+  static constexpr bool kApart = D != 128;
+  static constexpr int kState = kInfo + kWarps * 2 * 16;                  // [kWarps][1 or 2][8][2] floats: M, l
+  static constexpr int kMerge = kState + kWarps * (kApart ? 2 : 1) * 64;  // [kWarps][G][D] floats: first records' sums
   static constexpr size_t bytes(int G) { return kMerge + (size_t)kWarps * G * D * 4; }
+  // (a kilobyte a block is the system's)
+  static_assert(blocks_per_sm(D) * (kMerge + kWarps * TQ_PAGED_MAX_GQA * D * 4 + 1024) <= 228 * 1024, "blocks an SM");
 };
 
 // c += a b, and d = a b, for m16n8k16 fp16 operands.
@@ -209,6 +216,12 @@ struct Cursor {
     }
   }
 };
+
+// A warp that gives up still waits for its own copies: records will take their place.
+__device__ __noinline__ void give_up(uint64_t *bars, int used, int asked, unsigned int *errors) {
+  if ((threadIdx.x & 31) == 0) atomicOr(errors, TQ_ERRF_DECODE_WAIT);
+  for (int i = used; i < asked; ++i) mbar_wait(&bars[i % kStages], (i / kStages) & 1);
+}
 
 template <int D, class T>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kernel(const __grid_constant__ PagedDecodeArgs a) {
@@ -436,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       const int s = used % kStages;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], (used / kStages) & 1, a.c.wait_ns))) {
         dead = true;
-        if (lane == 0) atomicOr(a.c.errors, TQ_ERRF_DECODE_WAIT);
+        give_up(bars, a.c.withhold ? asked : used, asked, a.c.errors);
         break;
       }
       if (bad_stage >> s & 1u) {
@@ -639,10 +652,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     if (bad || dead) ps[0] = ps[1] = __int_as_float(0x7fffffff);
     const int ends = (here.step == 0 ? 1 : 0) | (here.step + end - at == here.steps ? 2 : 0);
     const int slot = 2 * warp + (at == begin ? 0 : 1);
-    // the last record's sums lie in the warp's own ring, whose copies have all been used
-    // (or its l is NaN: a copy that a warp gave up waiting for may still land there)
+    // the last record lies in the warp's own ring, whose copies have all landed and been used
     float *const rec = at == begin ? merge + (size_t)warp * G * D : reinterpret_cast<float *>(ring);
-    float *const rec_state = state + slot * 16;
+    float *const rec_state = S::kApart ? state + slot * 16 : at == begin ? state + warp * 16 : rec + G * D;
     if (ends != 3) {
       __syncwarp();
       if (g == 0)
@@ -676,9 +688,6 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     at = end;
     if (at < stop) here.settle(a.c);
   }
-  // a warp that gave up still waits for its own copies
-  if (dead && !a.c.withhold)
-    for (int i = used; i < asked; ++i) mbar_wait(&bars[i % kStages], (i / kStages) & 1);
 
   // ---- the block joins its warps' records: runs of one unit, in order
   __syncthreads();
@@ -703,7 +712,9 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       auto sums = [&](int k) {
         return k & 1 ? reinterpret_cast<const float *>(smem + (k / 2) * kStages * S::kStage) : merge + (size_t)(k / 2) * G * D;
       };
-      auto states = [&](int k) { return state + k * 16 + 2 * h; };
+      auto states = [&](int k) {
+        return (S::kApart ? state + k * 16 : k & 1 ? sums(k) + G * D : state + (k / 2) * 16) + 2 * h;
+      };
       for (int k = r; k <= last; ++k)
         if (info[k].place >= 0) top = fmaxf(top, states(k)[0]);
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
