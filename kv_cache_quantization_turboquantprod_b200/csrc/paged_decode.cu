@@ -42,8 +42,13 @@
 //    kept apart, both sums grow with the context and cancel at the end, and the
 //    tensor cores' truncating additions show: 1.7e-3 of the output at 131072
 //    tokens.)  sum p is one more product (A = ones).  bf16 outputs take p, p
-//    scale_j and p zero_j in fp16 (2^-12 each against the output's own 2^-9);
-//    fp16 outputs take them in two fp16 parts (22 bits).
+//    scale_j and p zero_j in fp16 (2^-11 each against the output's own 2^-8);
+//    fp16 outputs take them in two fp16 parts (22 bits), and the codes moved up
+//    to multiples of 2^-18: the tensor cores align a subnormal operand's product
+//    as if the operand were 2^-14, so a code at 2^-24 loses ten bits of the 24
+//    (2.4e-4 off in an output of 1.0 where values reach 4; at 2^-18 the output's
+//    rounding is all that shows; 16 x 32768 tokens at d = 256 88 -> 91 us, d = 128
+//    142 -> 143).  bf16 outputs and the scores do not see those bits.
 // mma.sync carries them: 18 products of 16 x 8 x 16 and 4 of half the depth a
 // cell keep its tensor pipe busy for less than half of the time that the bytes
 // take, and the operands come from registers without a trip through tensor memory.  (Queries as A with
@@ -437,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     // ps: sum p of heads 2 t and 2 t + 1 (every row the same); M: heads 2 t and 2 t + 1
     float acc[2 * NG][4], ps[4] = {0.f, 0.f, 0.f, 0.f}, M[2] = {-kInf, -kInf};
     int E = -1;
-    constexpr uint32_t kOnes = 0x3c003c00u, kOnesEven = 0x00010001u, kOnesOdd = 0x00100010u;
+    constexpr uint32_t kOnes = 0x3c003c00u, kOnesEven = 0x00010001u, kOnesOdd = 0x00100010u, kOnesTwo = 0x04000400u;
 #pragma unroll
     for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
@@ -604,11 +609,14 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int j = jp * P + i + k;
-              const uint32_t u = w0[i + k], v = w1[i + k], us = u >> 8, vs = v >> 8;
+              const uint32_t u = w0[i + k], v = w1[i + k];
               uint32_t b0, b1;
               if constexpr (kTwoParts) {
                 const float2 s0 = unpack_half2(sc[k][0]), s1 = unpack_half2(sc[k][1]);
                 const float2 h0 = unpack_half2(ph[0]), h1 = unpack_half2(ph[1]), l0 = unpack_half2(pl[0]), l1 = unpack_half2(pl[1]);
+                // the codes as multiples of 2^-18
+                const uint32_t e0 = u << 6 & 0x03c003c0u, o0 = u << 2 & 0x03c003c0u, e2 = u >> 2 & 0x03c003c0u, o2 = u >> 6 & 0x03c003c0u;
+                const uint32_t e1 = v << 6 & 0x03c003c0u, o1 = v << 2 & 0x03c003c0u, e3 = v >> 2 & 0x03c003c0u, o3 = v >> 6 & 0x03c003c0u;
                 const float pt[4] = {h0.x + l0.x, h0.y + l0.y, h1.x + l1.x, h1.y + l1.y};
                 const float y[4] = {pt[0] * s0.x, pt[1] * s0.y, pt[2] * s1.x, pt[3] * s1.y};
                 const float2 z0 = unpack_half2(ze[k][0]), z1 = unpack_half2(ze[k][1]);
@@ -618,15 +626,18 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
                 b1 = pack_half2(y[2], y[3]);
                 const float2 r0 = unpack_half2(b0), r1 = unpack_half2(b1);
                 const uint32_t q0 = pack_half2(y[0] - r0.x, y[1] - r0.y), q1 = pack_half2(y[2] - r1.x, y[3] - r1.y);
-                mma16(acc[2 * j], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, q0, q1);
-                mma16(acc[2 * j + 1], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, q0, q1);
+                mma16(acc[2 * j], e0, o0, e1, o1, q0, q1);
+                mma16(acc[2 * j + 1], e2, o2, e3, o3, q0, q1);
+                mma16(acc[2 * j], e0, o0, e1, o1, b0, b1);
+                mma16(acc[2 * j + 1], e2, o2, e3, o3, b0, b1);
               } else {
                 b0 = mul_half2(ph[0], sc[k][0]);
                 b1 = mul_half2(ph[1], sc[k][1]);
                 zh[j] = fma_half2(ph[1], ze[k][1], ce ? fma_half2(ph[0], ze[k][0], zh[j]) : mul_half2(ph[0], ze[k][0]));
+                const uint32_t us = u >> 8, vs = v >> 8;
+                mma16(acc[2 * j], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
+                mma16(acc[2 * j + 1], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, b0, b1);
               }
-              mma16(acc[2 * j], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
-              mma16(acc[2 * j + 1], us & 0x000f000fu, us & 0x00f000f0u, vs & 0x000f000fu, vs & 0x00f000f0u, b0, b1);
             }
           }
         }
@@ -634,12 +645,13 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
 #pragma unroll
       for (int j = 0; j < NG; ++j) {
         if constexpr (kTwoParts) {
-          // high and low part in the two halves of k
-          const uint32_t h = pack_half2(zf[j].x, zf[j].y);
+          // high and low part in the two halves of k; 2^-18 = 2^-14 2^-4
+          const float zx = zf[j].x * 0.0625f, zy = zf[j].y * 0.0625f;
+          const uint32_t h = pack_half2(zx, zy);
           const float2 r = unpack_half2(h);
-          const uint32_t lo = pack_half2(zf[j].x - r.x, zf[j].y - r.y);
-          mma16(acc[2 * j], kOnesEven, kOnesOdd, kOnesEven, kOnesOdd, h, lo);
-          mma16(acc[2 * j + 1], kOnesEven, kOnesOdd, kOnesEven, kOnesOdd, h, lo);
+          const uint32_t lo = pack_half2(zx - r.x, zy - r.y);
+          mma16(acc[2 * j], kOnesTwo, kOnesTwo, kOnesTwo, kOnesTwo, h, lo);
+          mma16(acc[2 * j + 1], kOnesTwo, kOnesTwo, kOnesTwo, kOnesTwo, h, lo);
         } else {
           mma8(acc[2 * j], kOnesEven, kOnesOdd, zh[j]);
           mma8(acc[2 * j + 1], kOnesEven, kOnesOdd, zh[j]);
@@ -670,10 +682,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     for (int j = 0; j < NG; ++j) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float w = 16777216.f;
+        constexpr float w = kTwoParts ? 0x1p18f : 0x1p24f, w_odd = kTwoParts ? w : w * 0.0625f;
         if (2 * t + i < G) {
-          const float4 o = make_float4(acc[2 * j][i] * w, acc[2 * j][i + 2] * (w * 0.0625f), acc[2 * j + 1][i] * w,
-                                       acc[2 * j + 1][i + 2] * (w * 0.0625f));
+          const float4 o = make_float4(acc[2 * j][i] * w, acc[2 * j][i + 2] * w_odd, acc[2 * j + 1][i] * w,
+                                       acc[2 * j + 1][i + 2] * w_odd);
           if (ends != 3) {
             *reinterpret_cast<float4 *>(rec + (2 * t + i) * D + 32 * j + 4 * g) = o;
           } else {

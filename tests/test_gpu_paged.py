@@ -279,6 +279,44 @@ def test_decode_ranges(scale_k, scale_v, softmax):
     _check_decode(st, kv, q, out, 128 ** -0.5 if softmax is None else softmax)
 
 
+@pytest.mark.parametrize("d,h_q,h_kv,dtype", [(64, 4, 4, F16), (128, 8, 4, BF16), (256, 4, 2, BF16)])
+@pytest.mark.parametrize("spread", [False, True])
+def test_decode_more_units_than_ranges(d, h_q, h_kv, dtype, spread):
+    """More (sequence, KV head) units than blocks: few, many or no steps in a unit, one that spans many blocks, empty
+    sequences at both ends."""
+    rng = np.random.default_rng(3)
+    total = [0, 0, 1] + [int(x) for x in rng.integers(0, 40 if spread else 400, 290)] + [4000 if spread else 700, 0, 33, 0]
+    table, pages = _tables(rng, total, 32)
+    cache = tq.PagedCache(d, h_kv, 32, pages)
+    batch = tq.PagedBatch(_i32(total), torch.from_numpy(table).to(DEV))
+    g = torch.Generator(device=DEV).manual_seed(0)
+    k, v = (torch.randn(sum(total), h_kv, d, generator=g, device=DEV) for _ in range(2))
+    tq.tq_paged_append(cache, batch, _cu(total), k, v)
+    kc, vc = torch.zeros_like(k), torch.zeros_like(v)
+    tq.tq_paged_gather(cache, batch, _cu(total), kc, vc)
+    q = torch.randn(len(total), h_q, d, generator=g, device=DEV).to(dtype)
+    out = torch.full_like(q, 7.0)
+    ws = tq.paged_workspace_for(cache, batch, h_q)
+    ws.fill_(0xFF)
+    tq.tq_paged_decode_attention(cache, batch, q, out, ws)
+    at = 0
+    for b, n in enumerate(total):
+        if n == 0:
+            assert not out[b].any()
+            continue
+        kb, vb = (x[at : at + n].double().transpose(0, 1) for x in (kc, vc))
+        w = torch.softmax(q[b].double().view(h_kv, -1, d) @ kb.transpose(1, 2) * d ** -0.5, -1)
+        o, size = w @ vb, w @ vb.abs()
+        big = float((q[b].double().abs().view(h_kv, -1, d) @ kb.abs().transpose(1, 2)).max() * d ** -0.5)
+        tol = _decode_tolerance(_np(o), _np(size), float(vb.abs().max()), big, d, dtype)
+        assert (np.abs(_np(out[b].view(h_kv, -1, d)) - _np(o)) <= tol).all(), b
+        at += n
+    again = torch.zeros_like(out)
+    tq.tq_paged_decode_attention(cache, batch, q, again, ws)
+    assert torch.equal(out, again)
+    assert tq.tq_device_errors() == 0
+
+
 def test_decode_long_and_ragged():
     """Many splits: one long sequence among short ones, against float64 on the device."""
     total = (20000, 1, 700, 16, 5003)
