@@ -9,13 +9,13 @@
 // heads, 8192 tokens 433 us, 1270 TFLOP/s (78% of the rate of one large bf16
 // product; 510 us, the same share, under the power cap); d = 256, 16/8 heads,
 // 467 us, 1177 TFLOP/s; d = 64, 32/8 heads, where exponentials and hand-offs
-// bind, 327 us, 840 TFLOP/s.  Short: 512 tokens, 12/2 heads, 11.2 us, most of
+// bind, 327 us, 840 TFLOP/s.  Short: 512 tokens, 12/2 heads, 10.4 us, most of
 // it the launch, the first copies and the end.
 //
 // Rows.  A tile's 128 rows are (token, query head of the group) pairs of one
 // KV head: 128 / G tokens with their G heads, so K and V are read once for
 // the group and short prompts fill the tile.  A block walks the keys that its
-// one or two tiles see (struct Prompt: two shapes).
+// one or two tiles see (struct Prompt: three shapes).
 //
 // Roles.  Warp 0 has the TMA engine copy Q once and the K and V tiles through
 // a ring (128-byte swizzle, one box per 64 channels); warp 1 issues the
@@ -61,21 +61,23 @@ namespace {
 
 using namespace sm100;
 
-// A block's shape.  NQ = 2: two tiles share the keys, 128 a step, one S buffer
-// each (three for both at d = 64), one block an SM.  NQ = 1: one tile, 64 keys a
-// step, two S buffers, two blocks an SM (one at d = 256).
-template <int D, int NQ>
+// A block's shape.  NQ = 2, KT = 128: two tiles share the keys, 128 a step, one S
+// buffer each (three for both at d = 64), one block an SM.  NQ = 1: one tile, two
+// S buffers; KT = 64 keys a step and two blocks an SM (one at d = 256), or KT =
+// 128 and one block.
+template <int D, int NQ, int KT>
 struct Prompt {
-  static_assert(D < 256 || NQ == 1, "two tiles' O do not fit beside S");
+  static_assert(D < 256 || (NQ == 1 && KT == 64), "O does not fit beside S");
+  static_assert(NQ == 1 || KT == 128, "two tiles take 128 keys");
   static constexpr int kBufs = NQ == 2 && D == 64 ? 3 : 2;  // S buffers
   static constexpr bool kAhead = kBufs > NQ;        // a tile's scores may come before its last weights are used
-  static constexpr int kBlocks = NQ == 2 || D == 256 ? 1 : 2;  // blocks of an SM
-  static constexpr int kKeys = NQ == 2 ? 128 : 64;  // keys of a step
+  static constexpr int kBlocks = KT == 128 || D == 256 ? 1 : 2;  // blocks of an SM
+  static constexpr int kKeys = KT;
   static constexpr bool kHalves = kKeys == 128 && !kAhead;  // P is handed over in two halves
   static constexpr int kSlabs = D / 64;             // 64-channel boxes
   static constexpr int kQSlab = 128 * 128, kSlab = kKeys * 128;
   static constexpr int kQTile = kQSlab * kSlabs, kStage = kSlab * kSlabs;
-  static constexpr int kStages = D == 64 ? 8 : D == 128 ? (NQ == 2 ? 5 : 4) : 5;
+  static constexpr int kStages = D == 64 ? 8 : kBlocks == 2 ? 4 : 5;
   static constexpr int kThreads = 128 + 256 * NQ;
   static constexpr int kExchange = NQ * kQTile + kStages * kStage;  // [NQ][2][128] floats, [NQ][2][4] ints
   static constexpr int kBad = kExchange + NQ * (1024 + 32);  // [D] ints: the first key with a special value
@@ -91,7 +93,7 @@ struct Prompt {
   }
   // registers of a thread: copies and products, softmax; together at most what
   // the launch has (96, 80 or 168 a thread)
-  static constexpr int kFew = 40, kMany = NQ == 2 ? 104 : D == 256 ? 216 : 96;
+  static constexpr int kFew = 40, kMany = NQ == 2 ? 104 : kBlocks == 1 ? 216 : 96;
 };
 
 // 2^y for two y in [-inf, 9] (or NaN) without the exponential unit: y is cut
@@ -130,12 +132,12 @@ __device__ __forceinline__ int block_sequence(const int32_t *cu, int batch, int 
   return lo;
 }
 
-template <int D, class T, int NQ>
-__global__ void __launch_bounds__(Prompt<D, NQ>::kThreads, Prompt<D, NQ>::kBlocks)
+template <int D, class T, int NQ, int KT>
+__global__ void __launch_bounds__(Prompt<D, NQ, KT>::kThreads, Prompt<D, NQ, KT>::kBlocks)
     prompt_kernel(const __grid_constant__ PromptArgs a, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int units) {
-  using C = Prompt<D, NQ>;
-  constexpr int KT = C::kKeys, ST = C::kStages;
+  using C = Prompt<D, NQ, KT>;
+  constexpr int ST = C::kStages;
   constexpr bool kBf16 = __is_same(T, __nv_bfloat16);
   constexpr int NB = C::kBufs;
   extern __shared__ __align__(1024) uint8_t smem[];  // (the swizzle's atoms)
@@ -636,9 +638,9 @@ bool encode(CUtensorMap *map, const void *p, long long stride, int heads, int pe
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, class T, int NQ>
+template <int D, class T, int NQ, int KT>
 cudaError_t launch(const PromptArgs &a, cudaStream_t stream) {
-  using C = Prompt<D, NQ>;
+  using C = Prompt<D, NQ, KT>;
   const int G = a.h_q / a.h_kv, tpt = 128 / G;
   const long long units = a.T_q / (tpt * NQ) + (long long)a.batch;
   if (units * a.h_kv > 0x7fffffffll) return cudaErrorInvalidConfiguration;
@@ -649,7 +651,7 @@ cudaError_t launch(const PromptArgs &a, cudaStream_t stream) {
       !encode<D, T>(&k, none ? a.q : a.k, none ? a.q_stride : a.k_stride, none ? a.h_q : a.h_kv, 0, none ? a.T_q : a.T_k, C::kKeys) ||
       !encode<D, T>(&v, none ? a.q : a.v, none ? a.q_stride : a.v_stride, none ? a.h_q : a.h_kv, 0, none ? a.T_q : a.T_k, C::kKeys))
     return cudaErrorInvalidValue;
-  auto *kernel = prompt_kernel<D, T, NQ>;
+  auto *kernel = prompt_kernel<D, T, NQ, KT>;
   static std::atomic<int> allowed[kAttributeDevices];
   const cudaError_t e = allow_smem(kernel, C::kSmem, allowed);
   if (e != cudaSuccess) return e;
@@ -666,10 +668,23 @@ cudaError_t launch_d(const PromptArgs &a, cudaStream_t stream) {
   // (262), 1 x 2048 41 (43), 4 x 2048 154 (153), 8 x 1536 196 (187), 32 x 512
   // 167 (145); d = 64, fp16, where two tiles have a third score buffer: 2 x
   // 4096 194 (222), 8 x 1536 159 (164), 16 x 1024 172 (169), 32 x 512 139 (124).
+  // Few tiles: one tile a block and 128 keys a step, half as many steps one after
+  // the other.  Up to a tile an SM from 384 keys on (12/2 heads, bf16: 512 tokens
+  // 10.4 us for 11.4 with 64 keys a step, 300 tokens 9.4 both ways; 32/8 heads,
+  // 700 tokens, 184 tiles: 15.2 for 14.0), up to two from 1280 on (12/2 heads,
+  // 2400 tokens 27 for 39 with two tiles a block, 8/8 heads, 5000 tokens, 312
+  // tiles: 61 for 73; 7000 tokens, 440 tiles: 105 for 97; 32/8 heads, 1500
+  // tokens, 376 tiles: 35 for 27).
   if constexpr (D < 256) {
-    if (a.T_k >= (D == 64 ? 1280ll : 2048ll) * a.batch) return launch<D, T, 2>(a, stream);
+    int sms;
+    const cudaError_t e = device_sm_count(&sms);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (a.T_q / (128 / (a.h_q / a.h_kv)) + (long long)a.batch) * a.h_kv;
+    const long long few = a.T_k >= 1280ll * a.batch ? 2ll * sms : sms;
+    if (tiles <= few && a.T_k >= 384ll * a.batch) return launch<D, T, 1, 128>(a, stream);
+    if (a.T_k >= (D == 64 ? 1280ll : 2048ll) * a.batch) return launch<D, T, 2, 128>(a, stream);
   }
-  return launch<D, T, 1>(a, stream);
+  return launch<D, T, 1, 64>(a, stream);
 }
 
 }  // namespace

@@ -553,6 +553,35 @@ def test_prompt_two_tiles_of_unlike_lengths(d, h_q, h_kv, new, nk):
     assert tq.tq_device_errors() == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 8])
+@pytest.mark.parametrize("new,nk", [((1,), (2048,)), ((20,), (2100,)), ((300, 100), (170, 4000)), ((100, 700), (2177, 2305)),
+                                    ((129, 257, 31), (2049, 2300, 2048))])
+def test_prompt_two_tiles_with_many_heads(d, G, new, nk):
+    """The same with more tiles than two an SM, which blocks of two tiles take; a few of the heads are looked at."""
+    tiles = sum(new) // (128 // G) + len(new)
+    h_kv = 300 // tiles + 2
+    g = torch.Generator(device=DEV).manual_seed(d + G)
+    dt = BF16 if G == 1 else F16
+    q = torch.randn(sum(new), h_kv * G, d, generator=g, device=DEV).to(dt)
+    grow = torch.cat([torch.linspace(0.25, 8.0, m, device=DEV) for m in nk])[:, None, None]
+    k = (torch.randn(sum(nk), h_kv, d, generator=g, device=DEV) * grow).to(dt)
+    v = torch.randn(sum(nk), h_kv, d, generator=g, device=DEV).to(dt)
+    out = torch.full_like(q, 3.0)
+    tq.tq_prompt_attention(q, k, v, _cu(new), _cu(nk), out)
+    for h in (0, h_kv // 2, h_kv - 1):
+        _check_on_device(q[:, h * G : h * G + G], k[:, h : h + 1], v[:, h : h + 1], new, nk, out[:, h * G : h * G + G])
+    again = torch.zeros_like(q)
+    tq.tq_prompt_attention(q, k, v, _cu(new), _cu(nk), again)
+    assert torch.equal(out, again)
+    assert tq.tq_device_errors() == 0
+
+
+@pytest.mark.parametrize("d,h_q,h_kv", [(128, 20, 5), (64, 18, 18)])
+def test_prompt_special_values_with_many_heads(d, h_q, h_kv):
+    test_prompt_special_values_reach_only_who_sees_them(d, h_q, h_kv, BF16, True)
+
+
 def test_prompt_long_against_float64_on_device():
     d, h_q, h_kv, new, past = 128, 8, 2, (2000, 3, 1111), (0, 3000, 517)
     nk = [a + b for a, b in zip(new, past)]
