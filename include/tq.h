@@ -432,7 +432,9 @@ TQ_API tq_status tq_set_wait_limit_ns(unsigned long long ns);
  * (nonzero), the tensor-core kernels of later calls withhold one hand-off
  * that their other roles wait for (decode, paged decode, paged append and
  * prompt: their copies; quantize-append: the loaded key operand), so those bounded waits run out after the wait
- * limit and the failure reporting above can be observed.  Nothing faults:
+ * limit and the failure reporting above can be observed.  2: the copies are
+ * made, and a wait counts as run out while they are in flight (paged append;
+ * no other call changes).  Nothing faults:
  * every wait is bounded and each kernel returns.  Off by default.  Always
  * TQ_OK.
  */
@@ -598,7 +600,8 @@ TQ_API size_t tq_paged_bytes(int d, int h_kv, int page_tokens, int num_pages);
  * sizes, h_q not a multiple of h_kv, q without q_out), TQ_ERR_UNSUPPORTED (d,
  * page_tokens, rotary_dim, dtype, more than TQ_PAGED_MAX_GQA query heads a KV
  * head), TQ_ERR_CAPACITY (more than 2^30 tokens or positions).  A kernel whose
- * bounded wait runs out sets TQ_ERRF_QUANTIZE_WAIT and leaves tokens unwritten.
+ * bounded wait runs out sets TQ_ERRF_QUANTIZE_WAIT and leaves tokens unwritten
+ * (their rows of q_out and k_out too).
  */
 TQ_API tq_status tq_paged_append(const tq_paged_cache *c, const tq_paged_batch *s, const tq_rope *rope,
                                  const int32_t *cu_new, const void *q, const void *k, const void *v, tq_dtype dtype,

@@ -22,7 +22,7 @@ struct PagedView {
   int num_pages, h_kv;
   unsigned int *errors;
   unsigned long long wait_ns;  // limit of the bounded waits
-  int withhold;                // tests of the timeout path: no copies
+  int withhold;                // tests of the timeout path (tq_test_withhold_handoffs); 1: no copies
 };
 
 // Sections and strides of a cell of head dim D (bytes).

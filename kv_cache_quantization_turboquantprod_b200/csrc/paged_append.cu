@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) paged_append_kernel(con
   const int from = max(own, lo), count = max(min(own + kOwn, hi) - from, 0);
   __syncwarp();
   if (lane == 0 && count > 0) sm100::mbar_arrive_expect_tx(bar, (uint32_t)(count * row_elems * sizeof(T)));
-  if (lane < 3 * count && !a.c.withhold) {
+  if (lane < 3 * count && a.c.withhold != 1) {
     const int pos = from + lane / 3, kind = lane % 3;
     T *const to = rows + (pos - 16 * cell) * row_elems;
     const size_t row = (size_t)(r0 + (pos - first));
@@ -218,9 +218,14 @@ __global__ void __launch_bounds__(2 * D, 1024 / (2 * D)) paged_append_kernel(con
   const int page = page_of(a.c, b, lo);
   if (page < 0 && tid == 0) atomicOr(a.c.errors, TQ_ERRF_PAGE);
   if (live && !in_table && p == 0 && h == 0) atomicOr(a.c.errors, TQ_ERRF_POSITION);
-  // (a copy always lands; should a wait run out, the warp's rows stay unwritten)
-  const bool ok = count > 0 && __all_sync(0xffffffffu, sm100::mbar_wait(bar, 0, a.c.wait_ns));
-  if (count > 0 && !ok && lane == 0) atomicOr(a.c.errors, TQ_ERRF_QUANTIZE_WAIT);
+  // Should the wait run out, the warp's rows stay unwritten, and it waits for its copies before it leaves: the shared
+  // memory is the next block's then.  (withhold 1: no copies; 2: they count as late.)
+  const bool ok =
+      count > 0 && __all_sync(0xffffffffu, a.c.withhold != 2 && sm100::mbar_wait(bar, 0, a.c.wait_ns));
+  if (count > 0 && !ok) {
+    if (lane == 0) atomicOr(a.c.errors, TQ_ERRF_QUANTIZE_WAIT);
+    if (a.c.withhold != 1) sm100::mbar_wait(bar, 0);
+  }
 
   if (ok) {
     // ---- rotation: turns the chunks a and b of a head row

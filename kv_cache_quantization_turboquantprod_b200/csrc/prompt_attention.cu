@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ, KT>::kThreads, Prompt<D, NQ, KT>
           for (int s = 0; s < C::kSlabs; ++s)
             tma_load_4d(smem + x * C::kQTile + s * C::kQSlab, &qmap, 64 * s, 0, h, q0 + i0 + x * tpt, q_full);
         int item = 0;  // K and V tiles in turn
-        for (; item < (a.withhold ? 0 : 2 * most); ++item) {
+        for (; item < (a.withhold == 1 ? 0 : 2 * most); ++item) {
           const int st = item % ST;
           if (item >= ST && !pipe_wait(&kv_empty[st], (item / ST - 1) & 1, abort_flag, a.wait_ns, hint, &timed_out)) break;
           mbar_arrive_expect_tx(&kv_full[st], C::kStage);

@@ -94,7 +94,7 @@ cudaError_t set_wait_fields(Args &a) {
   const unsigned long long ns = g_wait_ns.load(std::memory_order_relaxed);
   a.wait_ns = ns;
   a.wait_hint_ns = (unsigned int)(ns < 1000000ull ? ns : 1000000ull);
-  a.test_withhold = g_withhold.load(std::memory_order_relaxed);
+  a.test_withhold = g_withhold.load(std::memory_order_relaxed) == 1;
   return error_word_address(&a.errors);
 }
 
@@ -436,7 +436,7 @@ tq_status tq_set_wait_limit_ns(unsigned long long ns) {
 }
 
 tq_status tq_test_withhold_handoffs(int on) {
-  g_withhold.store(on ? 1 : 0, std::memory_order_relaxed);
+  g_withhold.store(on == 2 ? 2 : on ? 1 : 0, std::memory_order_relaxed);
   return TQ_OK;
 }
 

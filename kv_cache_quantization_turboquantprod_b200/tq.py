@@ -434,10 +434,11 @@ def tq_set_wait_limit_ns(ns: int) -> None:
     _check("tq_set_wait_limit_ns", load().tq_set_wait_limit_ns(int(ns)))
 
 
-def tq_test_withhold_handoffs(on: bool) -> None:
+def tq_test_withhold_handoffs(on: bool | int) -> None:
     """Tests of the timeout path: make later calls' tensor-core kernels
-    withhold one hand-off so that their bounded waits run out."""
-    _check("tq_test_withhold_handoffs", load().tq_test_withhold_handoffs(int(bool(on))))
+    withhold one hand-off so that their bounded waits run out (2: see
+    include/tq.h)."""
+    _check("tq_test_withhold_handoffs", load().tq_test_withhold_handoffs(int(on)))
 
 
 def tq_test_sign_refine_threshold(z: float) -> None:
