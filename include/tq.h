@@ -433,8 +433,9 @@ TQ_API tq_status tq_set_wait_limit_ns(unsigned long long ns);
  * that their other roles wait for (decode, paged decode, paged append and
  * prompt: their copies; quantize-append: the loaded key operand), so those bounded waits run out after the wait
  * limit and the failure reporting above can be observed.  2: the copies are
- * made, and a wait counts as run out while they are in flight (paged append;
- * no other call changes).  Nothing faults:
+ * made, and a wait counts as run out while they are in flight (paged append),
+ * or runs out in one of two warps that go on together (prompt; no other call
+ * changes).  Nothing faults:
  * every wait is bounded and each kernel returns.  Off by default.  Always
  * TQ_OK.
  */

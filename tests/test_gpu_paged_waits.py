@@ -84,3 +84,64 @@ def test_append_that_gives_up_waits_for_its_copies(hook, d, h_q, h_kv, dtype, ro
         for i in (0, 2):
             assert torch.equal(worlds[i][0].buffer, want) and torch.equal(rows_out[i], want_rows)
     assert tq.tq_device_errors(clear=True) == tq.ERRF_QUANTIZE_WAIT
+
+
+def _prompt_inputs(d, h_q, h_kv, dtype, n, step=64):
+    """Keys that are small in the first step and large behind it, so that the running maximum moves at the second."""
+    g = torch.Generator(device=DEV).manual_seed(d + n)
+    q = (1.5 * torch.randn(n, h_q, d, generator=g, device=DEV)).to(dtype)
+    size = torch.where(torch.arange(n, device=DEV) < step, 0.25, 12.0)
+    k = (torch.randn(n, h_kv, d, generator=g, device=DEV) * size[:, None, None]).to(dtype)
+    return q, k, torch.randn(n, h_kv, d, generator=g, device=DEV).to(dtype)
+
+
+def _many(tiles_a_head):
+    """KV heads that give more than two tiles an SM."""
+    return 2 * torch.cuda.get_device_properties(0).multi_processor_count // tiles_a_head + 1
+
+
+PROMPT = [
+    # d, h_q / h_kv, h_kv (None: many tiles), dtype, tokens, keys of a step, tokens of a tile whose rows see one step only
+    (64, 1, 2, BF16, 100, 64, 0),       # the failing step is the last one
+    (128, 2, 2, F16, 100, 64, 64),
+    (256, 1, 1, BF16, 120, 64, 0),
+    (128, 1, 2, BF16, 200, 64, 0),      # more steps behind it
+    (128, 1, 2, F16, 500, 128, 128),    # 128 keys a step, one tile
+    (64, 1, None, BF16, 1400, 128, 0),  # two tiles, three score buffers
+]
+
+
+@pytest.mark.parametrize("d,group,h_kv,dtype,n,step,whole", PROMPT)
+def test_prompt_wait_that_runs_out_for_one_half_of_a_row(hook, d, group, h_kv, dtype, n, step, whole):
+    """A wait for the tile's products that runs out in one of a row's two threads: both leave, the call returns, and no row is
+    finite and wrong (tiles of one step wait for no product)."""
+    h_kv = h_kv or _many(n // (128 // group) + 1)
+    q, k, v = _prompt_inputs(d, group * h_kv, h_kv, dtype, n, step)
+    cu = _cu([n])
+    clean = torch.full_like(q, 3.0)
+    tq.tq_prompt_attention(q, k, v, cu, cu, clean)
+    assert torch.isfinite(clean).all() and tq.tq_device_errors() == 0
+    out = torch.full_like(q, 3.0)
+    tq.tq_set_wait_limit_ns(2_000_000)
+    hook(2)
+    tq.tq_prompt_attention(q, k, v, cu, cu, out)
+    assert tq.tq_device_errors(clear=True) == tq.ERRF_PROMPT_WAIT
+    nan = torch.isnan(out).all(-1)
+    assert nan[whole:].all() and not nan[:whole].any()
+    assert torch.equal(out[:whole], clean[:whole])
+    hook(0)
+    tq.tq_set_wait_limit_ns(0)
+    tq.tq_prompt_attention(q, k, v, cu, cu, out)
+    assert torch.equal(out, clean) and tq.tq_device_errors() == 0
+
+
+@pytest.mark.parametrize("d,h_q,h_kv,n", [(64, 2, 2, 300), (128, 8, 2, 1000), (256, 2, 1, 200)])
+def test_prompt_without_its_copies_is_nan(hook, d, h_q, h_kv, n):
+    q, k, v = _prompt_inputs(d, h_q, h_kv, BF16, n)
+    cu = _cu([n])
+    out = torch.full_like(q, 3.0)
+    tq.tq_set_wait_limit_ns(2_000_000)
+    hook(1)
+    tq.tq_prompt_attention(q, k, v, cu, cu, out)
+    assert tq.tq_device_errors(clear=True) == tq.ERRF_PROMPT_WAIT
+    assert torch.isnan(out).all()
