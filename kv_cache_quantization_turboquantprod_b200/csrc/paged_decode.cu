@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     const int s = asked % kStages, first = kStep * next.step, have = min(cells - first, kStep);
     const bool bad = (uint32_t)page0 >= (uint32_t)a.c.num_pages || (!joined && (uint32_t)page1 >= (uint32_t)a.c.num_pages);
     bad_stage = (bad_stage & ~(1u << s)) | ((uint32_t)bad << s);
-    if (lane == 0 && a.c.withhold != 1) {
+    if (lane == 0 && !a.c.withhold) {
       uint8_t *const to = ring + s * S::kStage;
       const uint8_t *const from = a.c.data + (size_t)page0 * page_bytes + (size_t)next.h * head_bytes;
       if (bad) {
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
       const int s = used % kStages;
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], (used / kStages) & 1, a.c.wait_ns))) {
         dead = true;
-        give_up(bars, a.c.withhold == 1 ? asked : used, asked, a.c.errors);
+        give_up(bars, a.c.withhold ? asked : used, asked, a.c.errors);
         break;
       }
       if (bad_stage >> s & 1u) {

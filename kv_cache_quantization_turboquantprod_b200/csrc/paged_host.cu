@@ -169,6 +169,7 @@ tq_status tq_paged_decode_attention(const tq_paged_cache *c, const tq_paged_batc
   if (tq::device_sm_count(&a.num_sms) != cudaSuccess) return TQ_ERR_CUDA;
   if (workspace_bytes < tq::paged_decode_workspace(c->d, c->h_kv, h_q, s->batch, a.num_sms)) return TQ_ERR_WORKSPACE;
   if ((st = view(c, s, &a.c)) != TQ_OK) return st;
+  a.c.withhold = a.c.withhold == 1;  // (decided here: the test of it in the kernel's loop cost 2%)
   a.q = q; a.out = out; a.q_stride = q_stride; a.out_stride = out_stride;
   a.h_q = h_q; a.scale_log2 = softmax_scale * kLog2e;
   a.partials = static_cast<float *>(workspace);
