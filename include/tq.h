@@ -645,6 +645,11 @@ TQ_API size_t tq_paged_decode_workspace_size(const tq_paged_cache *c, int batch,
  *   workspace  device, tq_paged_decode_workspace_size() bytes, 256-byte
  *              aligned, no initialisation; one per call in flight
  * A sequence with no tokens gets a zero row, one with a bad page NaN rows.
+ * Sums are float32; weights and their products with scales and zeros are fp16
+ * (two parts of it for fp16 outputs), relative to the largest weight and, where
+ * groups of 32 channels differ much, to each group's largest value: an output
+ * channel is off by the roundings of its own group's values and by some 2^-22 of
+ * the largest of them, whatever the other groups hold.
  * Lengths beyond max_pages * page_tokens are bad pages.  softmax_scale times
  * log2(e) must be finite; logits beyond 2^24, which float32 does not resolve
  * to a softmax, may give NaN.  A kernel whose bounded wait runs out writes NaN

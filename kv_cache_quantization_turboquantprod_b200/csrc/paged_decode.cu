@@ -58,7 +58,17 @@
 // Softmax.  Weights are 2^(x - M) with a running reference M per head that
 // only has to keep p, p scale_j and p zero_j in fp16's range, and a bound E of
 // the scales' and zeros' exponents; both move (and the accumulators with them) when a token
-// exceeds them, which one vote a step (two cells) finds out.
+// exceeds them, which one vote a step (two cells) finds out.  One bound serves
+// groups within 2^8 of each other.  Where a step shows groups further apart, p
+// scale_j of the small ones would fall below fp16's normal range (2048 tokens,
+// values of 4000 beside 0.001: 5% rms in bf16 outputs, 6% in fp16, where it is 0.3
+// and 0.04 now, the outputs' own rounding); from there on every
+// group has its own bound E_j, its scales and zeros are brought to 2^6 in
+// shared memory before they are used, each step anew, and its accumulators
+// hold units of 2^(E_j - 6).  An output is then off, beside its roundings, by
+// some 2^-22 of the largest value of its own group.  (2^-E_j on p for each group
+// and cell instead, always or in a second copy of the products, took 4% more time
+// of every call.)
 #include "paged.cuh"
 #include "sm100.cuh"
 #include "tq_common.cuh"
@@ -73,6 +83,9 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kStep = 2;    // cells of a step
 constexpr int kStages = 2;  // steps in a warp's ring
 constexpr float kTop = 9.f, kSlack = 4.f;  // p 2^E <= 2^9 when M moves, < 2^13 always (four p zero_j stay below 2^16)
+// The least bound E (p stays in fp16's range); groups whose bounds lie further than kSpan apart are brought to
+// 2^kCommon each, and the lanes' E holds E_j - kApart (below every e, so that each step finds its way there).
+constexpr int kLeast = -2, kSpan = 8, kCommon = 6, kApart = 1000;
 
 __host__ __device__ constexpr int blocks_per_sm(int d) { return d == 256 ? 1 : 2; }
 
@@ -441,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     // acc[2 j + i]: channels 32 j + 4 g + 2 i (rows g) and + 1 (rows g + 8), heads 2 t and 2 t + 1;
     // ps: sum p of heads 2 t and 2 t + 1 (every row the same); M: heads 2 t and 2 t + 1
     float acc[2 * NG][4], ps[4] = {0.f, 0.f, 0.f, 0.f}, M[2] = {-kInf, -kInf};
-    int E = -1;
+    int E = kLeast;  // of all groups; groups apart: E_j - kApart of group g % NG
+    auto unit_of = [](int e) { return e < kLeast ? e + kApart - kCommon : 0; };  // exponent of the unit of acc[2 j], acc[2 j + 1]
     constexpr uint32_t kOnes = 0x3c003c00u, kOnesEven = 0x00010001u, kOnesOdd = 0x00100010u, kOnesTwo = 0x04000400u;
 #pragma unroll
     for (int i = 0; i < 2 * NG; ++i)
@@ -546,10 +560,35 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
           far = max3f(far, p[ce][i], p[ce][i + 1]);
         }
       if (__any_sync(0xffffffffu, far > kTop + kSlack - (float)E || e > E)) {
+        const bool were_apart = E < kLeast;
+        e = max(max(e, __shfl_xor_sync(0xffffffffu, e, 1)), kLeast);
+        e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+        const int all = max(__reduce_max_sync(0xffffffffu, e), E);
+        const bool apart = __any_sync(0xffffffffu, were_apart || all - e > kSpan);
+        const int to_e = apart ? max(e - kApart, E < kLeast ? E : -kApart + kLeast) : all;
+        const float shift = (float)(apart ? kCommon : all), up = shift - (float)(were_apart ? kCommon : E);
+        if (apart) {
+          const int unit = unit_of(to_e);
+          const float ratio = __int_as_float((127 + unit_of(E) - unit) << 23);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-        const float up = (float)(max(e, E) - E);
-        E = max(e, E);
+          for (int j = 0; j < NG; ++j) {
+            const float f = __shfl_sync(0xffffffffu, ratio, 4 * j);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[2 * j + k / 4][k % 4] *= f;
+          }
+          // the step's value scales and zeros, each lane those of a group
+          const int j = lane % NG;
+          const __half f = __float2half_rn(__int_as_float((127 - __shfl_sync(0xffffffffu, unit, 4 * j)) << 23));
+          for (int n = lane / NG; n < kStep * kCell; n += 32 / NG) {
+            uint8_t *const at = stage + (n / kCell) * C::kBytes + C::scale_at(n % kCell, j);
+            __half *const s = reinterpret_cast<__half *>(at + C::kValScale), *const z = reinterpret_cast<__half *>(at + C::kValZero);
+            *s = __hmul(*s, f);
+            *z = __hmul(*z, f);
+          }
+          fence_proxy_async_smem();  // before a later copy into this stage
+          __syncwarp();
+        }
+        E = to_e;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float big = -kInf;
@@ -559,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
             for (int o = 0; o < 2; ++o) big = none[ce][o] ? big : fmaxf(big, c1[i] * x[ce][2 * o + i]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-          const float to = fmaxf(big - kTop + (float)E, M[i] + up);
+          const float to = fmaxf(big - kTop + shift, M[i] + up);
           const float f = M[i] == -kInf ? 0.f : exp2f(M[i] - to);
           M[i] = to;
           ps[i] *= f;
@@ -680,9 +719,10 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(D)) paged_decode_kerne
     }
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
+      const float w = __int_as_float((127 + (kTwoParts ? 18 : 24) + unit_of(__shfl_sync(0xffffffffu, E, 4 * j))) << 23);
+      const float w_odd = kTwoParts ? w : w * 0.0625f;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        constexpr float w = kTwoParts ? 0x1p18f : 0x1p24f, w_odd = kTwoParts ? w : w * 0.0625f;
         if (2 * t + i < G) {
           const float4 o = make_float4(acc[2 * j][i] * w, acc[2 * j][i + 2] * w_odd, acc[2 * j + 1][i] * w,
                                        acc[2 * j + 1][i + 2] * w_odd);
