@@ -1,5 +1,6 @@
 """The paged decode against its 64-bit definition, channel by channel, within the bounds of paged_bounds (test_paged_bounds shows
-that these see a lost token, a shifted tail and a wrong scale): groups of unlike sizes and tokens of unlike sizes."""
+that these see a lost token, a shifted tail and a wrong scale): ordinary data, groups of unlike sizes, tokens of unlike sizes, and
+the number of sequences at which the splitting changes."""
 
 import numpy as np
 import pytest
@@ -94,6 +95,15 @@ def _query(seed, B, h_q, d, dtype, size):
     return (size * torch.randn(B, h_q, d, generator=g)).to(dtype).to(DEV)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("d,h_q,h_kv,page,total", [(128, 8, 2, 16, (1, 15, 16, 17, 0, 257)), (64, 8, 1, 32, (333, 2, 48)),
+                                                   (256, 6, 3, 64, (70, 150)), (128, 5, 5, 128, (64, 129, 200))])
+@pytest.mark.parametrize("size", [0.375, 1.5])
+def test_ordinary_values(d, h_q, h_kv, page, total, dtype, size):
+    w = World(*_data(d, total, h_kv, d), d, h_kv, page, total)
+    print("share of the bound", w.check(_query(1, len(total), h_q, d, dtype, size)))
+
+
 UNLIKE = [(1000.0, 0.1), (1000.0, 0.01), (4000.0, 0.01), (4000.0, 0.001), (0.001, 20000.0), (1e-4, 1.0, 1e3, 1e-2)]
 
 
@@ -121,3 +131,25 @@ def test_tokens_of_unlike_sizes(d, dtype):
             y[a:, :, 32 * j : 32 * j + 32] = rng.standard_normal((700 - a, 2, 32)) * s
     w = World(x, y, d, 2, 16, total)
     print("share of the bound", w.check(_query(3, 1, 8, d, dtype, 0.75)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("scale_k,scale_v,softmax", [(1e-3, 1e-3, None), (30.0, 300.0, None), (1.0, 1e-5, 0.5), (8.0, 1.0, -0.3),
+                                                     (1.0, 1.0, 0.0)])
+def test_ranges(scale_k, scale_v, softmax, dtype):
+    total = (77, 200)
+    w = World(*_data(11, total, 2, 128, (scale_v,), scale_k), 128, 2, 32, total)
+    print("share of the bound", w.check(_query(4, 2, 8, 128, dtype, 1.0), softmax))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("B", [255, 256, 257, 296, 297])
+def test_one_head_of_as_many_sequences_as_threads_and_blocks(B, dtype):
+    """One KV head and some 256 sequences (a block's threads) or 296 (two blocks an SM): where the prefix sums take a second round
+    and the joining changes its form."""
+    rng = np.random.default_rng(B)
+    total = [int(n) for n in rng.integers(0, 70, B)]
+    total[B // 2] = 3000  # one that many ranges share
+    w = World(*_data(B, total, 1, 64), 64, 1, 16, total)
+    units = {(b, 0) for b in list(range(0, B, 17)) + [B // 2 - 1, B // 2, B // 2 + 1, 255, 256, B - 2, B - 1]}
+    print("share of the bound", w.check(_query(6, B, 2, 64, dtype, 0.375), units=units))
