@@ -573,7 +573,7 @@ typedef struct {
  */
 TQ_API tq_status tq_make_rope_table(int max_positions, int rotary_dim, double theta, float *table);
 
-/* Bytes of a page pool, or 0 for bad arguments. */
+/* Bytes of a page pool, or 0 for bad arguments (more than 64 bits hold among them: TQ_ERR_CAPACITY of the calls). */
 TQ_API size_t tq_paged_bytes(int d, int h_kv, int page_tokens, int num_pages);
 
 /*

@@ -19,12 +19,19 @@ bool rows_ok(const void *p, long long stride, long long row, tq_dtype t) {
   return p && aligned(p, 16) && stride >= row && (size_t)stride * dtype_size(t) % 16 == 0;
 }
 
+// Bytes of a pool of valid arguments; false where they are more than an address holds.
+bool pool_bytes(int d, int h_kv, int page_tokens, int num_pages, size_t *out) {
+  const size_t cells = (size_t)num_pages * h_kv, cell = (size_t)(page_tokens / 16) * 20 * d;
+  return !__builtin_mul_overflow(cells, cell, out);
+}
+
 tq_status check_cache(const tq_paged_cache *c) {
   if (!c || !c->data || !aligned(c->data, 256)) return TQ_ERR_INVALID_ARGUMENT;
   if (!head_dim_ok(c->d)) return TQ_ERR_UNSUPPORTED;
   if (c->page_tokens < 16 || c->page_tokens > 1024 || (c->page_tokens & (c->page_tokens - 1))) return TQ_ERR_UNSUPPORTED;
   if (c->h_kv < 1 || c->num_pages < 1) return TQ_ERR_INVALID_ARGUMENT;
-  return TQ_OK;
+  size_t bytes;
+  return pool_bytes(c->d, c->h_kv, c->page_tokens, c->num_pages, &bytes) ? TQ_OK : TQ_ERR_CAPACITY;
 }
 
 tq_status check_batch(const tq_paged_cache *c, const tq_paged_batch *s) {
@@ -83,7 +90,8 @@ tq_status tq_make_rope_table(int max_positions, int rotary_dim, double theta, fl
 size_t tq_paged_bytes(int d, int h_kv, int page_tokens, int num_pages) {
   if (!head_dim_ok(d) || h_kv < 1 || num_pages < 1) return 0;
   if (page_tokens < 16 || page_tokens > 1024 || (page_tokens & (page_tokens - 1))) return 0;
-  return (size_t)num_pages * h_kv * (page_tokens / 16) * 20 * d;
+  size_t bytes;
+  return pool_bytes(d, h_kv, page_tokens, num_pages, &bytes) ? bytes : 0;
 }
 
 tq_status tq_paged_append(const tq_paged_cache *c, const tq_paged_batch *s, const tq_rope *rope, const int32_t *cu_new,
