@@ -504,7 +504,7 @@ def _token_rows(name: str, t: torch.Tensor, heads: int, d: int, dtype, device, r
     stride, by_head, by_channel = t.stride()
     if by_channel != 1 or (by_head != d and heads > 1):
         raise ValueError(f"{name}: a token's heads must be contiguous rows")
-    return stride if rows > 1 else max(stride, heads * d)
+    return stride if rows > 1 else heads * d  # (one row's stride means nothing)
 
 
 def _three_dims(name: str, t: torch.Tensor):

@@ -25,3 +25,14 @@ def test_pools_beyond_an_address(d, h_kv, page, pages, fits):
     assert lib.tq_paged_decode_workspace_size(pool(), 2, 32) == 0
     with pytest.raises(tq.TQError):
         tq.PagedCache(d, h_kv, page, pages, buffer=torch.zeros(16, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("stride", [0, 7, 129, 1027])
+def test_one_row_has_no_stride(stride):
+    """A single token's rows count as packed, whatever lies between it and a next one."""
+    x = torch.zeros(4096, dtype=torch.bfloat16)
+    one = x.as_strided((1, 2, 64), (stride, 64, 1))
+    assert tq._token_rows("k", one, 2, 64, torch.bfloat16, x.device, 1) == 128
+    assert tq._token_rows("k", x.as_strided((0, 2, 64), (stride, 64, 1)), 2, 64, torch.bfloat16, x.device, 0) == 128
+    two = x.as_strided((2, 2, 64), (stride, 64, 1))
+    assert tq._token_rows("k", two, 2, 64, torch.bfloat16, x.device, 2) == stride
