@@ -473,14 +473,6 @@ __global__ void __launch_bounds__(Prompt<D, NQ, KT>::kThreads, Prompt<D, NQ, KT>
       // The maximum moves only where it grew by more than 2^8 (from -inf to
       // anything; not from -inf to -inf).
       if (named_bar_or(pair_bar, 64, (top - m) * c > 8.f || !ok)) {
-        // (O is about to change: its last product first, or the scores were issued behind it.  Before the exchange, so
-        // that both threads of a row go on, or neither does.)
-        if (C::kAhead && j > 0 && ok) {
-          ok = wait(&o_done[x], (j - 1) & 1);
-          // (a test of the timeout path: a wait that runs out for one of the row's two threads)
-          if (ok && a.withhold == 2 && part) ok = wait(&o_done[x], j & 1);
-          tc_fence_after();
-        }
         exchange[mine_at] = top;
         if (lane == 0) exchange_ok[(2 * x + part) * 4 + quarter] = ok;
         named_bar_sync(pair_bar, 64);
@@ -492,9 +484,17 @@ __global__ void __launch_bounds__(Prompt<D, NQ, KT>::kThreads, Prompt<D, NQ, KT>
         const float f = was == m ? 1.f : ex2_approx((was - m) * c);  // was = -inf: 0
         l *= f;
         if (j > 0) {
+          // O's last product first (or the scores were issued behind it).  Should this run out, the warp leaves O and goes
+          // on, so that its partner finds it at the barriers: the abort flag is up, and no row of the block comes from O.
+          bool there = true;
+          if constexpr (C::kAhead) {
+            there = wait(&o_done[x], (j - 1) & 1);
+            if (a.withhold == 2 && part) there = wait(&o_done[x], j & 1);  // a test of that: not before P is handed over
+            tc_fence_after();
+          }
           const uint32_t ot = tmem + C::o_col(x) + lanes + part * DH;
 #pragma unroll 1
-          for (int i = 0; i < DH; i += 32) {
+          for (int i = 0; i < DH && there; i += 32) {
             uint32_t o[32];
             tmem_ld32(ot + i, o);
             tmem_wait_ld();
@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(Prompt<D, NQ, KT>::kThreads, Prompt<D, NQ, KT>
       l += exchange[other_at];
       // (not o_done: by now it may stand one or two products behind the last,
       // and a parity cannot tell the last but one from the one after the last)
-      // Where a role has given up, products may be missing before it.
+      // Where a role has given up, products may be missing before it, or O have changed under one.
       if (most > 0) ok = wait(drained, 0) && __all_sync(0xffffffffu, *abort_flag == 0);
     }
     tc_fence_after();
