@@ -652,7 +652,8 @@ TQ_API size_t tq_paged_decode_workspace_size(const tq_paged_cache *c, int batch,
  * the largest of them, whatever the other groups hold.
  * Lengths beyond max_pages * page_tokens are bad pages.  softmax_scale times
  * log2(e) must be finite; logits beyond 2^24, which float32 does not resolve
- * to a softmax, may give NaN.  A kernel whose bounded wait runs out writes NaN
+ * to a softmax, may give NaN, and rows of queries whose largest value is below
+ * 2^-126 (bf16 only) count as zero queries.  A kernel whose bounded wait runs out writes NaN
  * rows and sets TQ_ERRF_DECODE_WAIT.
  */
 TQ_API tq_status tq_paged_decode_attention(const tq_paged_cache *c, const tq_paged_batch *s, const void *q,

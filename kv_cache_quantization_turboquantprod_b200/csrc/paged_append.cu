@@ -21,8 +21,11 @@
 // words and half words that no other token shares.
 //
 // Bound: the rows' and pages' bytes on paper; measured, instruction issue (the
-// float64 products of the rotation, their conversions, the codes).  4 x 8192
-// tokens, 32/8 heads, d = 128, bf16: 797 MB in 192 us, 4.15 TB/s (a thread per
+// float64 products of the rotation, their conversions, the codes; in a capture
+// issue 69% of the cycles, the conversion unit and the ALU 48% each; at 32/8
+// heads 32 of 40 turned rows are queries).  4 x 8192
+// tokens, 32/8 heads, d = 128, bf16: 797 MB in 193 us, 4.1 TB/s (fp32: 1535 MB in
+// 229 us, the copy rate; bf16 with a thread per
 // 16 channels with its rows in registers: 266; a warp per cell with the rare
 // exact codes inlined: 738, out of the instruction cache).  23 ragged fp16
 // sequences, 12/2 heads, d = 64: 12.4 us.  One token of 32 sequences: 6.0 us,

@@ -3,11 +3,15 @@
 // Bound: the pages' bytes (1.25 d per token and KV head).  At the measured
 // copy rate an SM receives one cell (16 tokens of a KV head, 20 d bytes) every
 // ~110 cycles at d = 128, so a warp scheduler has ~440 issue slots a cell; a
-// warp takes ~310 instructions for one, and issue is what remains as the bound.
-// Measured, d = 128, 32/8 heads, bf16: 16 sequences of 16-32K tokens 102 us,
-// 5.25 TB/s (80% of the copy rate); 32 of them 210 us, 4 x 131072 tokens 142 us
-// (4.8 and 4.7 TB/s, under the power cap); fp16 (two parts of p) 142 us for the
-// 16.  Short work is latency: 1 x 4096 tokens 11.6 us, 61 sequences of up to
+// warp takes ~310 instructions for one.  In a capture issue is active in 58% of
+// the cycles, the ALU pipe in 53%, the tensor pipe in 33%, at 3.6 warps a
+// scheduler: what remains beside the bytes is the dependent latency of a warp's
+// own chain, with no registers or shared memory for more warps.
+// Measured, 32/8 heads, 16 sequences of 16-32K tokens: d = 128, bf16 102 us, 5.25
+// TB/s (80% of the copy rate), fp16 (two parts of p) 143; d = 64 73 (56%: a step
+// has half the bytes and 0.7 of the instructions) and 99; d = 256, 16/4 heads, 94
+// (87%) and 139.  32 such sequences at d = 128 180 us, 4 x 131072 tokens 123 (212
+// and 142 under the power cap).  Short work is latency: 1 x 4096 tokens 11.3 us, 61 sequences of up to
 // 1500 tokens at d = 256 23 us in bf16, 26 in fp16.
 //
 // Split.  All steps (pairs of cells) of the batch, in the order (sequence, KV

@@ -8,8 +8,11 @@
 // that it takes, one of 64 keys in 48 for 32).  Measured, bf16: d = 128, 32/8
 // heads, 8192 tokens 433 us, 1270 TFLOP/s (78% of the rate of one large bf16
 // product; 510 us, the same share, under the power cap); d = 256, 16/8 heads,
-// 467 us, 1177 TFLOP/s; d = 64, 32/8 heads, where exponentials and hand-offs
-// bind, 327 us, 840 TFLOP/s.  Short: 512 tokens, 12/2 heads, 10.4 us, most of
+// where products of 64 keys bind, 467 us, 1177 TFLOP/s; d = 64, 32/8 heads, 327
+// us, 840 TFLOP/s.  In captures (d = 128, 256, 64) the tensor pipe is busy 63, 57
+// and 39% of the cycles, the exponential unit 56, 25 and 69%, issue 49, 29 and 58%:
+// at d = 64 exponentials come first, and waits for tensor memory and hand-offs
+// keep their unit from filling.  Short: 512 tokens, 12/2 heads, 10.4 us, most of
 // it the launch, the first copies and the end.
 //
 // Rows.  A tile's 128 rows are (token, query head of the group) pairs of one
@@ -673,6 +676,9 @@ cudaError_t launch_d(const PromptArgs &a, cudaStream_t stream) {
   // (262), 1 x 2048 41 (43), 4 x 2048 154 (153), 8 x 1536 196 (187), 32 x 512
   // 167 (145); d = 64, fp16, where two tiles have a third score buffer: 2 x
   // 4096 194 (222), 8 x 1536 159 (164), 16 x 1024 172 (169), 32 x 512 139 (124).
+  // The host knows the sums and not the lengths, so one long prompt among short
+  // ones gets the shape of the average (8192 tokens and fifteen of 16, d = 128: 490
+  // us, the 8192 alone, with two tiles a block, 451).
   // Few tiles: one tile a block and 128 keys a step, half as many steps one after
   // the other.  Up to a tile an SM from 384 keys on (12/2 heads, bf16: 512 tokens
   // 10.4 us for 11.4 with 64 keys a step, 300 tokens 9.4 both ways; 32/8 heads,
