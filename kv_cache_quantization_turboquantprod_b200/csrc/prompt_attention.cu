@@ -12,7 +12,7 @@
 // us, 840 TFLOP/s.  In captures (d = 128, 256, 64) the tensor pipe is busy 63, 57
 // and 39% of the cycles, the exponential unit 56, 25 and 69%, issue 49, 29 and 58%:
 // at d = 64 exponentials come first, and waits for tensor memory and hand-offs
-// keep their unit from filling.  Short: 512 tokens, 12/2 heads, 10.4 us, most of
+// keep their unit from filling.  Short: 512 tokens, 12/2 heads, 9.9 us, most of
 // it the launch, the first copies and the end.
 //
 // Rows.  A tile's 128 rows are (token, query head of the group) pairs of one
